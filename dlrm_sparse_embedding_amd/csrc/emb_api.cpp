@@ -13,12 +13,15 @@
 
 #include "emb.h"
 #include "emb_internal.h"
+#include "seq_internal.h"
 
 using namespace emb;
 
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
+
+namespace emb {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -38,6 +41,10 @@ int ok() {
 int hip_fail(hipError_t e, const char* what) {
   return fail(EMB_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace emb
+
+namespace {
 
 struct TimedLaunch {
   int kid;

@@ -1,0 +1,368 @@
+// Rotary positions, the per-head norm of queries and keys with the rotation in
+// the same pass, its gradient, and the append of keys and values to a paged
+// cache with both applied on the way.
+//
+// Mathematics. A head x of dim elements, pairs (a_i, b_i) among its first rot:
+//   forward   y = R(x r w),  r = (mean x^2 + eps)^(-1/2),  R = turn by pos f_i, times mag
+//   gradient  u = R^T dy,  n = x r,  dx = r (u w - n mean(u w n)),  dw = sum u n
+// All of it is one pass over the heads: bound by memory. Angles are integers:
+// pair i's frequency is a 64-bit fraction of a turn, so position * frequency
+// modulo 2^64 is exact however far the position is; sine and cosine come from
+// the Taylor series on an eighth of a turn to either side of a quadrant's
+// middle (terms to x^9 and x^10, truncation below 5e-9).
+//
+// Layout. A lane owns one "unit": 2 V elements (V = 16 bytes' worth) that hold
+// V whole pairs, as two 16-byte accesses: V elements at p and V at p + rot/2
+// (half layout) or p + V (interleaved), so one set of sines serves a unit in
+// either layout. The lanes of a head are a power of two of neighbours, so the
+// norm's sum is a few lane exchanges. Operands that 16-byte accesses do not
+// fit go through the element-wise kernels below.
+#include <algorithm>
+
+#include "emb_device.h"
+#include "seq_internal.h"
+
+namespace emb {
+
+namespace {
+
+template <int DT>
+struct Elem {
+  using T = uint16_t;
+};
+template <>
+struct Elem<EMB_F32> {
+  using T = float;
+};
+
+template <int DT>
+__device__ __forceinline__ float ld1(const void* p, long long i) {
+  if constexpr (DT == EMB_F32) return reinterpret_cast<const float*>(p)[i];
+  else return half_to_f32<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void st1(void* p, long long i, float x) {
+  if constexpr (DT == EMB_F32) reinterpret_cast<float*>(p)[i] = x;
+  else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_half<DT>(x);
+}
+
+// Conversions of the vector paths: the hardware's, to nearest even with
+// subnormals kept (the default mode of these kernels).
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 hf2 __attribute__((ext_vector_type(2)));
+typedef float fl2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ void widen(const u4 v, float* out) {
+  if constexpr (DT == EMB_F16) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const hf2 h = __builtin_bit_cast(hf2, w[i]);
+      out[2 * i] = (float)h.x;
+      out[2 * i + 1] = (float)h.y;
+    }
+  } else {
+    widen16<DT>(v, out);
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ u4 narrow(const float* in) {
+  if constexpr (DT == EMB_F32) {
+    return u4{__float_as_uint(in[0]), __float_as_uint(in[1]), __float_as_uint(in[2]), __float_as_uint(in[3])};
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const fl2 f = {in[2 * i], in[2 * i + 1]};
+      if constexpr (DT == EMB_BF16) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2));
+      else w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, hf2));
+    }
+    return u4{w[0], w[1], w[2], w[3]};
+  }
+}
+
+// Sine and cosine of pos * turn / 2^64 turns. The phase's upper 32 bits are
+// kept (2^-32 of a turn); what is left after the nearest quarter is at most an
+// eighth of a turn.
+__device__ __forceinline__ void sincos_turn(uint64_t turn, long long pos, float mag, float* c, float* s) {
+  const uint32_t ph = (uint32_t)((turn * (uint64_t)pos) >> 32);
+  const uint32_t quad = (ph + 0x20000000u) >> 30;
+  const float x = (float)(int)(ph - (quad << 30)) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  const float sn = x + x * z * (-1.f / 6 + z * (1.f / 120 + z * (-1.f / 5040 + z * (1.f / 362880))));
+  const float cs = 1.f + z * (-0.5f + z * (1.f / 24 + z * (-1.f / 720 + z * (1.f / 40320 + z * (-1.f / 3628800)))));
+  const float a = (quad & 1) ? sn : cs;  // |cos|
+  const float b = (quad & 1) ? cs : sn;  // |sin|
+  *c = ((quad + 1) & 2) ? -mag * a : mag * a;
+  *s = (quad & 2) ? -mag * b : mag * b;
+}
+
+__device__ __forceinline__ long long position(const void* p, int itype, long long t) {
+  return itype == EMB_I64 ? reinterpret_cast<const long long*>(p)[t] : (long long)reinterpret_cast<const int*>(p)[t];
+}
+
+// Sum over the lanes of a group of G neighbours (G a power of two).
+__device__ __forceinline__ float group_sum(float x, int G) {
+  for (int d = 1; d < G; d <<= 1) x += __shfl_xor(x, d, 64);
+  return x;
+}
+
+// ---- element by element ------------------------------------------------------
+// One wave for each head; lane l owns pairs l, l + 64, .. and the elements
+// behind the rotation. Right for every dim, rot, stride and alignment.
+
+// Pair i's two elements.
+__device__ __forceinline__ void pair_at(const RotTable& rot, int i, int* ea, int* eb) {
+  if (rot.layout == EMB_ROT_HALF) {
+    *ea = i;
+    *eb = i + rot.rot / 2;
+  } else {
+    *ea = 2 * i;
+    *eb = 2 * i + 1;
+  }
+}
+
+// y = rotate(x [* r * w]) for one head, by one wave.
+template <int DT>
+__device__ void head_any(const void* x, long long xi, void* y, long long yi, int dim, const RotTable& rot,
+                         long long pos, float sign, bool norm, const float* w, float eps) {
+  const int lane = threadIdx.x & 63;
+  float r = 1.f;
+  if (norm) {
+    float ss = 0.f;
+    for (int e = lane; e < dim; e += 64) {
+      const float v = ld1<DT>(x, xi + e);
+      ss += v * v;
+    }
+    r = 1.f / sqrtf(group_sum(ss, 64) / (float)dim + eps);
+  }
+  for (int i = lane; i < rot.rot / 2; i += 64) {
+    int ea, eb;
+    pair_at(rot, i, &ea, &eb);
+    float c, s;
+    sincos_turn(rot.turn[i], pos, rot.mag, &c, &s);
+    s *= sign;
+    const float a = ld1<DT>(x, xi + ea) * r * (w ? w[ea] : 1.f);
+    const float b = ld1<DT>(x, xi + eb) * r * (w ? w[eb] : 1.f);
+    st1<DT>(y, yi + ea, a * c - b * s);
+    st1<DT>(y, yi + eb, a * s + b * c);
+  }
+  for (int e = rot.rot + lane; e < dim; e += 64) {
+    if (norm) {
+      st1<DT>(y, yi + e, ld1<DT>(x, xi + e) * r * (w ? w[e] : 1.f));
+    } else {
+      using T = typename Elem<DT>::T;
+      reinterpret_cast<T*>(y)[yi + e] = reinterpret_cast<const T*>(x)[xi + e];
+    }
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_norm_rotary_any(NormRotaryArgs a, RotTable rot) {
+  const int H = a.q.n + a.k.n;
+  for (long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); item < a.tokens * H;
+       item += (long long)gridDim.x * 4) {
+    const long long t = item / H;
+    const int h = (int)(item - t * H);
+    const bool isq = h < a.q.n;
+    const Heads& in = isq ? a.q : a.k;
+    const Heads& out = isq ? a.qo : a.ko;
+    const int hh = isq ? h : h - a.q.n;
+    head_any<DT>(in.p, t * in.ts + hh * in.hs, const_cast<void*>(out.p), t * out.ts + hh * out.hs, a.dim, rot,
+                 position(a.positions, a.itype, t), a.inverse ? -1.f : 1.f, a.norm, isq ? a.wq : a.wk, a.eps);
+  }
+}
+
+// Gradient, element by element. Each wave takes heads in turn; it sums the
+// weights' gradients of its heads in LDS, the block's waves are joined at the
+// end in their order.
+template <int DT>
+__global__ __launch_bounds__(256) void k_norm_rotary_back_any(NormRotaryBackArgs a, RotTable rot) {
+  extern __shared__ float s_dw[];  // [4][2][dim]
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int dim = a.dim;
+  for (int i = threadIdx.x; i < 8 * dim; i += 256) s_dw[i] = 0.f;
+  __syncthreads();
+  const int H = a.q.n + a.k.n;
+  for (long long item = (long long)blockIdx.x * 4 + wave; item < a.tokens * H; item += (long long)gridDim.x * 4) {
+    const long long t = item / H;
+    const int h = (int)(item - t * H);
+    const bool isq = h < a.q.n;
+    const int hh = isq ? h : h - a.q.n;
+    const Heads& in = isq ? a.q : a.k;
+    const Heads& dy = isq ? a.dyq : a.dyk;
+    const Heads& dx = isq ? a.dq : a.dk;
+    const float* w = isq ? a.wq : a.wk;
+    float* dw = s_dw + (wave * 2 + (isq ? 0 : 1)) * dim;
+    const long long xi = t * in.ts + hh * in.hs, yi = t * dy.ts + hh * dy.hs, oi = t * dx.ts + hh * dx.hs;
+    const long long pos = position(a.positions, a.itype, t);
+    float ss = 0.f;
+    for (int e = lane; e < dim; e += 64) {
+      const float v = ld1<DT>(in.p, xi + e);
+      ss += v * v;
+    }
+    const float r = 1.f / sqrtf(group_sum(ss, 64) / (float)dim + a.eps);
+    // twice over the head: first the mean of u w n, then the gradient
+    float dot = 0.f;
+    for (int pass = 0; pass < 2; ++pass) {
+      const float mean = pass ? group_sum(dot, 64) / (float)dim : 0.f;
+      auto one = [&](int e, float u) {
+        const float n = ld1<DT>(in.p, xi + e) * r;
+        const float g = u * (w ? w[e] : 1.f);
+        if (pass == 0) {
+          dot += g * n;
+        } else {
+          dw[e] += u * n;  // element e is this lane's alone
+          st1<DT>(const_cast<void*>(dx.p), oi + e, r * (g - n * mean));
+        }
+      };
+      for (int i = lane; i < rot.rot / 2; i += 64) {
+        int ea, eb;
+        pair_at(rot, i, &ea, &eb);
+        float c, s;
+        sincos_turn(rot.turn[i], pos, rot.mag, &c, &s);
+        const float da = ld1<DT>(dy.p, yi + ea), db = ld1<DT>(dy.p, yi + eb);
+        const float ua = da * c + db * s, ub = db * c - da * s;
+        one(ea, ua);
+        one(eb, ub);
+      }
+      for (int e = rot.rot + lane; e < dim; e += 64) one(e, ld1<DT>(dy.p, yi + e));
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * dim; i += 256) {
+    float s = 0.f;
+    for (int w = 0; w < 4; ++w) s += s_dw[w * 2 * dim + i];
+    a.part[(long long)blockIdx.x * 2 * dim + i] = s;
+  }
+}
+
+// Weights' gradients from the blocks' partial sums, in 64 bits: 4 columns for
+// each block, 64 lanes down the blocks for each column.
+__global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int blocks, int dim,
+                                                 float* __restrict__ dwq, float* __restrict__ dwk) {
+  __shared__ double s[256];
+  const int col = blockIdx.x * 4 + (threadIdx.x & 3);
+  const int row = threadIdx.x >> 2;
+  double acc = 0.0;
+  if (col < 2 * dim)
+    for (int b = row; b < blocks; b += 64) acc += (double)part[(long long)b * 2 * dim + col];
+  s[threadIdx.x] = acc;
+  __syncthreads();
+  for (int d = 32; d >= 1; d >>= 1) {
+    if (row < d) s[threadIdx.x] += s[threadIdx.x + 4 * d];
+    __syncthreads();
+  }
+  if (row == 0 && col < 2 * dim) {
+    float* out = col < dim ? dwq : dwk;
+    if (out) out[col < dim ? col : col - dim] = (float)s[threadIdx.x];
+  }
+}
+
+// ---- the append -----------------------------------------------------------------
+
+// The sequence of token t: the last b with offsets[b] <= t.
+__device__ __forceinline__ int seq_of(const int* offsets, int seqs, int t) {
+  int lo = 0, hi = seqs;  // offsets[lo] <= t < offsets[hi] by contract
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (offsets[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int div_by(const FastDiv d, int n) {
+  return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
+}
+
+// Page and slot in it of token t; false where it has none. *slot is the slot
+// in the sequence.
+__device__ __forceinline__ bool place(const AppendArgs& a, int t, int* page, int* in_page, int* slot) {
+  int b = t, first = t, n = 1;
+  if (a.offsets) {
+    b = seq_of(a.offsets, a.seqs, t);
+    first = a.offsets[b];
+    n = a.offsets[b + 1] - first;
+    if (t < first || t >= first + n) {  // offsets that do not cover the token
+      if (a.kv.error) atomicOr(a.kv.error, kKvBadOffsets);
+      return false;
+    }
+  }
+  const long long s = (long long)a.lens[b] - n + (t - first);
+  if (s < 0 || s >= (long long)a.width * a.kv.page) {
+    if (a.kv.error) atomicOr(a.kv.error, kKvBadPage);
+    return false;
+  }
+  const int col = div_by(a.kv.by_page, (int)s);
+  const int p = a.table[(long long)b * a.width + col];
+  if (p < 0 || p >= a.kv.pages) {
+    if (a.kv.error) atomicOr(a.kv.error, kKvBadPage);
+    return false;
+  }
+  *page = p;
+  *in_page = (int)s - col * a.kv.page;
+  *slot = (int)s;
+  return true;
+}
+
+template <int DT>
+__global__ __launch_bounds__(256) void k_append_any(AppendArgs a, RotTable rot) {
+  const int H = 2 * a.kv.heads;
+  const KvView& kv = a.kv;
+  for (long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); item < a.tokens * H;
+       item += (long long)gridDim.x * 4) {
+    const long long t = item / H;
+    const int h = (int)(item - t * H);
+    int page, in_page, slot;
+    if (!place(a, (int)t, &page, &in_page, &slot)) continue;
+    if (h < kv.heads) {
+      const long long pos = a.positions ? position(a.positions, a.itype, t) : (long long)slot;
+      head_any<DT>(a.k.p, t * a.k.ts + h * a.k.hs, kv.k, page * kv.kps + in_page * kv.kss + h * kv.khs, kv.dim, rot,
+                   pos, 1.f, a.norm, a.wk, a.eps);
+    } else {
+      using T = typename Elem<DT>::T;
+      const int hv = h - kv.heads;
+      const T* src = reinterpret_cast<const T*>(a.v.p) + t * a.v.ts + hv * a.v.hs;
+      T* dst = reinterpret_cast<T*>(kv.v) + (page * kv.vps + in_page * kv.vss + hv * kv.vhs);
+      for (int e = threadIdx.x & 63; e < kv.dim; e += 64) dst[e] = src[e];
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_norm_rotary(const NormRotaryArgs& a, const RotTable& rot, hipStream_t st) {
+  const long long items = a.tokens * (a.q.n + a.k.n);
+  const unsigned grid = (unsigned)std::min<long long>((items + 3) / 4, 1 << 20);
+  if (a.dtype == EMB_F32) k_norm_rotary_any<EMB_F32><<<grid, 256, 0, st>>>(a, rot);
+  else if (a.dtype == EMB_BF16) k_norm_rotary_any<EMB_BF16><<<grid, 256, 0, st>>>(a, rot);
+  else k_norm_rotary_any<EMB_F16><<<grid, 256, 0, st>>>(a, rot);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_rotary_back(const NormRotaryBackArgs& a, const RotTable& rot, hipStream_t st) {
+  const int blocks = norm_rotary_back_blocks(a.tokens, a.q.n, a.k.n, a.dim);
+  if (blocks > 0) {
+    const size_t lds = 8 * sizeof(float) * a.dim;
+    if (a.dtype == EMB_F32) k_norm_rotary_back_any<EMB_F32><<<blocks, 256, lds, st>>>(a, rot);
+    else if (a.dtype == EMB_BF16) k_norm_rotary_back_any<EMB_BF16><<<blocks, 256, lds, st>>>(a, rot);
+    else k_norm_rotary_back_any<EMB_F16><<<blocks, 256, lds, st>>>(a, rot);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (a.dwq || a.dwk) k_norm_dw<<<(2 * a.dim + 3) / 4, 256, 0, st>>>(a.part, blocks, a.dim, a.dwq, a.dwk);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_append(const AppendArgs& a, const RotTable& rot, hipStream_t st) {
+  const long long items = a.tokens * 2 * a.kv.heads;
+  const unsigned grid = (unsigned)std::min<long long>((items + 3) / 4, 1 << 20);
+  if (a.kv.dtype == EMB_F32) k_append_any<EMB_F32><<<grid, 256, 0, st>>>(a, rot);
+  else if (a.kv.dtype == EMB_BF16) k_append_any<EMB_BF16><<<grid, 256, 0, st>>>(a, rot);
+  else k_append_any<EMB_F16><<<grid, 256, 0, st>>>(a, rot);
+  return hipGetLastError();
+}
+
+}  // namespace emb

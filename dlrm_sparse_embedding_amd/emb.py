@@ -70,6 +70,31 @@ class emb_table_desc(ctypes.Structure):
                 ("master", ctypes.c_void_p * EMB_MAX_SLICES)]
 
 
+EMB_ROT_HALF, EMB_ROT_INTERLEAVED = 0, 1
+EMB_ROT_NONE, EMB_ROT_LINEAR, EMB_ROT_BASE, EMB_ROT_PARTS, EMB_ROT_BANDS = 0, 1, 2, 3, 4
+EMB_MAX_ROT = 256
+EMB_MAX_HEAD_DIM = 1024
+ROT_LAYOUT = {"half": EMB_ROT_HALF, "interleaved": EMB_ROT_INTERLEAVED}
+ROT_SCALING = {"none": EMB_ROT_NONE, "linear": EMB_ROT_LINEAR, "base": EMB_ROT_BASE, "parts": EMB_ROT_PARTS,
+               "bands": EMB_ROT_BANDS}
+_HEADS_DTYPE = {torch.float32: EMB_F32, torch.bfloat16: EMB_BF16, torch.float16: EMB_F16}
+
+
+class emb_rotary_desc(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("turns_low", ctypes.c_double), ("turns_high", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class emb_kv_desc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_page_stride", ctypes.c_int64), ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("page", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("error", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -138,6 +163,35 @@ def lib() -> ctypes.CDLL:
     L.emb_probe_reads.restype = ctypes.c_int
     L.emb_probe_update.argtypes = [vp, i64, vp, vp, i64, i32, vp]
     L.emb_probe_update.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    heads_io = [vp, i64, i64]
+    L.emb_create_rotary.argtypes = [ctypes.POINTER(emb_rotary_desc), ctypes.POINTER(vp)]
+    L.emb_create_rotary.restype = ctypes.c_int
+    L.emb_destroy_rotary.argtypes = [vp]
+    L.emb_destroy_rotary.restype = None
+    both = (heads_io * 2 + [i32]) * 2
+    L.emb_rotary_apply.argtypes = [vp, vp, i32, i64, i32, i32] + both + [i32, vp]
+    L.emb_rotary_apply.restype = ctypes.c_int
+    L.emb_qk_norm_rotary.argtypes = [vp, vp, i32, i64, i32, i32] + both + [vp, vp, f32, vp]
+    L.emb_qk_norm_rotary.restype = ctypes.c_int
+    L.emb_qk_norm_rotary_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    L.emb_qk_norm_rotary_workspace_bytes.restype = sz
+    L.emb_qk_norm_rotary_backward.argtypes = ([vp, vp, i32, i64, i32, i32] + (heads_io * 3 + [i32]) * 2 +
+                                              [vp, vp, f32, vp, sz, vp, vp, vp])
+    L.emb_qk_norm_rotary_backward.restype = ctypes.c_int
+    L.emb_create_kv.argtypes = [ctypes.POINTER(emb_kv_desc), ctypes.POINTER(vp)]
+    L.emb_create_kv.restype = ctypes.c_int
+    L.emb_destroy_kv.argtypes = [vp]
+    L.emb_destroy_kv.restype = None
+    L.emb_check_kv_error.argtypes = [vp, vp]
+    L.emb_check_kv_error.restype = ctypes.c_int
+    L.emb_kv_append.argtypes = [vp, vp, i64, i32, i32, i32] + heads_io * 2 + [vp, i32, vp, vp, i32, vp, i32, i32, vp, f32, vp]
+    L.emb_kv_append.restype = ctypes.c_int
+    L.emb_prefix_attention_workspace_bytes.argtypes = [vp, i64, i32, i32, i32, i32]
+    L.emb_prefix_attention_workspace_bytes.restype = sz
+    L.emb_prefix_attention.argtypes = [vp, i64, i32, i32] + heads_io * 2 + [i32, f32, vp, i32, vp, vp, i32, vp, i32, vp, vp, i32,
+                                                                  vp, sz, vp, vp]
+    L.emb_prefix_attention.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -350,6 +404,250 @@ def emb_kernel_times(ctx: int) -> dict:
     n = (ctypes.c_int64 * len(KERNELS))()
     _check(lib().emb_kernel_times(ctx, ms, n))
     return {k: (ms[i], int(n[i])) for i, k in enumerate(KERNELS)}
+
+
+# ---- sequence operators --------------------------------------------------------
+
+def _dtype_code(name: str, t: torch.Tensor) -> int:
+    code = _HEADS_DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} is {t.dtype}: fp32, bf16 or fp16")
+    return code
+
+
+def _heads(name: str, t: torch.Tensor, tokens: int, dim: int, dtype: torch.dtype):
+    """Checks a [tokens, heads, dim] operand; its (pointer, token stride, head stride)."""
+    if t.dim() != 3 or t.shape[0] != tokens or t.shape[2] != dim:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not [{tokens}, heads, {dim}]")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not in device memory")
+    ts, hs, es = t.stride()
+    if es != 1 and dim > 1:
+        raise ValueError(f"the elements of one head of {name} must be contiguous")
+    return t.data_ptr(), ts, hs
+
+
+def _dense(name: str, t: torch.Tensor, dtype, shape):
+    """Checks a contiguous device tensor of known type and shape; its pointer."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous device memory")
+    return t.data_ptr()
+
+
+def _weight(name: str, w, dim: int):
+    return None if w is None else _dense(name, w, torch.float32, (dim,))
+
+
+def _positions(positions: torch.Tensor, tokens: int):
+    return _dense("positions", positions, positions.dtype, (tokens,)), _itype(positions)
+
+
+def _workspace(ws: torch.Tensor):
+    if not ws.is_cuda:
+        raise ValueError("ws is not in device memory")
+    return _ptr(ws), ws.numel() * ws.element_size()
+
+
+def _io(q, q_out, k, k_out):
+    """The operands of a call over queries and, where given, keys."""
+    T, hq, D = q.shape
+    code = _dtype_code("q", q)
+    args = [*_heads("q", q, T, D, q.dtype), *_heads("q_out", q_out, T, D, q.dtype), hq]
+    if q_out.shape[1] != hq:
+        raise ValueError(f"q_out has {q_out.shape[1]} heads, q {hq}")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        args += [None, 0, 0, None, 0, 0, 0]
+    else:
+        if k_out is None or k_out.shape[1] != k.shape[1]:
+            raise ValueError("k_out must have k's heads")
+        args += [*_heads("k", k, T, D, q.dtype), *_heads("k_out", k_out, T, D, q.dtype), k.shape[1]]
+    return T, D, code, args
+
+
+def emb_create_rotary(desc: emb_rotary_desc) -> int:
+    out = ctypes.c_void_p()
+    _check(lib().emb_create_rotary(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def emb_destroy_rotary(rot: int) -> None:
+    lib().emb_destroy_rotary(rot)
+
+
+def emb_rotary_apply(rot: int, positions, q, q_out, k=None, k_out=None, inverse: bool = False, stream=None) -> None:
+    """q, k: [tokens, heads, dim], any strides over tokens and heads; positions: int32 or int64 [tokens].
+    q_out may be q, k_out k."""
+    T, D, code, args = _io(q, q_out, k, k_out)
+    pos, itype = _positions(positions, T)
+    _check(lib().emb_rotary_apply(rot, pos, itype, T, code, D, *args, 1 if inverse else 0, _stream(stream)))
+
+
+def emb_qk_norm_rotary(rot: int, positions, q, q_out, k, k_out, wq, wk, eps: float, stream=None) -> None:
+    """wq, wk: fp32 [dim] or None; k and k_out may be None."""
+    T, D, code, args = _io(q, q_out, k, k_out)
+    pos, itype = _positions(positions, T)
+    _check(lib().emb_qk_norm_rotary(rot, pos, itype, T, code, D, *args, _weight("wq", wq, D), _weight("wk", wk, D),
+                                    float(eps), _stream(stream)))
+
+
+def emb_qk_norm_rotary_workspace_bytes(tokens: int, q_heads: int, k_heads: int, dim: int) -> int:
+    return int(lib().emb_qk_norm_rotary_workspace_bytes(int(tokens), int(q_heads), int(k_heads), int(dim)))
+
+
+def emb_qk_norm_rotary_backward(rot: int, positions, q, dyq, dq, k, dyk, dk, wq, wk, eps: float, ws, dwq=None,
+                                dwk=None, stream=None) -> None:
+    """Gradients of emb_qk_norm_rotary: dq, dk (may be dyq, dyk) and, where given, dwq and dwk (fp32 [dim])."""
+    T, D, code, args = _io(q, dq, k, dk)
+    hq, hk = args[6], args[13]
+    if dyq.shape[1] != hq or (k is not None and (dyk is None or dyk.shape[1] != hk)):
+        raise ValueError("dyq and dyk must have the heads of q and k")
+    gq = _heads("dyq", dyq, T, D, q.dtype)
+    gk = _heads("dyk", dyk, T, D, q.dtype) if k is not None else (None, 0, 0)
+    pos, itype = _positions(positions, T)
+    ws_p, ws_n = _workspace(ws)
+    _check(lib().emb_qk_norm_rotary_backward(
+        rot, pos, itype, T, code, D, *args[0:3], *gq, *args[3:7], *args[7:10], *gk, *args[10:14],
+        _weight("wq", wq, D), _weight("wk", wk, D), float(eps), ws_p, ws_n, _weight("dwq", dwq, D),
+        _weight("dwk", dwk, D), _stream(stream)))
+
+
+def emb_create_kv(desc: emb_kv_desc) -> int:
+    out = ctypes.c_void_p()
+    _check(lib().emb_create_kv(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def emb_destroy_kv(kv: int) -> None:
+    lib().emb_destroy_kv(kv)
+
+
+def emb_check_kv_error(kv: int, stream=None) -> None:
+    _check(lib().emb_check_kv_error(kv, _stream(stream)))
+
+
+def _sequences(T: int, offsets, lens, table):
+    B = lens.shape[0]
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs, pages]")
+    width = table.shape[1]
+    return (None if offsets is None else _dense("offsets", offsets, torch.int32, (B + 1,)), B,
+            _dense("lens", lens, torch.int32, (B,)), _dense("table", table, torch.int32, (B, width)), width)
+
+
+def emb_kv_append(kv: int, rot, k, v, offsets, lens, table, wk=None, eps=None, positions=None, stream=None) -> None:
+    """Appends k, v [tokens, heads, dim] to their sequences' pages. offsets: int32 [seqs + 1], or None for one token
+    each; lens: int32 [seqs], with the new tokens; table: int32 [seqs, pages]. rot: a rotation's handle or None;
+    positions: int32 or int64 [tokens], or None for the slots. Keys are normed where wk is given, or where eps is
+    given and not 0."""
+    T, D = k.shape[0], k.shape[2]
+    if v.shape[1] != k.shape[1]:
+        raise ValueError("k and v must have the same heads")
+    pos, itype = (None, EMB_I64) if positions is None else _positions(positions, T)
+    norm = wk is not None or bool(eps)
+    _check(lib().emb_kv_append(kv, rot, T, _dtype_code("k", k), k.shape[1], D, *_heads("k", k, T, D, k.dtype), *_heads("v", v, T, D, k.dtype),
+                               *_sequences(T, offsets, lens, table), pos, itype, 1 if norm else 0,
+                               _weight("wk", wk, D), float(eps or 0.0), _stream(stream)))
+
+
+def emb_prefix_attention_workspace_bytes(kv: int, tokens: int, q_heads: int, groups: int, prefix_width: int,
+                                         table_width: int) -> int:
+    return int(lib().emb_prefix_attention_workspace_bytes(kv, int(tokens), int(q_heads), int(groups),
+                                                          int(prefix_width), int(table_width)))
+
+
+def emb_prefix_attention(kv: int, q, out, scale: float, offsets, lens, table, group_offsets, prefix_lens,
+                         prefix_table, ws, lse=None, stream=None) -> None:
+    """q, out: [tokens, q_heads, dim] of the cache's type. offsets, lens, table: as emb_kv_append; group_offsets
+    (int32 [groups + 1], over sequences), prefix_lens (int32 [groups]) and prefix_table (int32 [groups, pages]), or
+    all None. lse: fp32 [tokens, q_heads] or None."""
+    T, hq, D = q.shape
+    if out.shape[1] != hq:
+        raise ValueError(f"out has {out.shape[1]} heads, q {hq}")
+    if prefix_lens is None:
+        if group_offsets is not None or prefix_table is not None:
+            raise ValueError("group_offsets, prefix_lens and prefix_table go together")
+        groups = (None, 0, None, None, 0)
+    else:
+        G = prefix_lens.shape[0]
+        if prefix_table.dim() != 2:
+            raise ValueError("prefix_table must be [groups, pages]")
+        width = prefix_table.shape[1]
+        groups = (_dense("group_offsets", group_offsets, torch.int32, (G + 1,)), G,
+                  _dense("prefix_lens", prefix_lens, torch.int32, (G,)),
+                  _dense("prefix_table", prefix_table, torch.int32, (G, width)), width)
+    ws_p, ws_n = _workspace(ws)
+    _check(lib().emb_prefix_attention(
+        kv, T, _dtype_code("q", q), D, *_heads("q", q, T, D, q.dtype), *_heads("out", out, T, D, q.dtype), hq, float(scale),
+        *_sequences(T, offsets, lens, table), *groups, ws_p, ws_n,
+        None if lse is None else _dense("lse", lse, torch.float32, (T, hq)), _stream(stream)))
+
+
+class Rotary:
+    """A rotation: the first `rot` elements of each head, in the "half" or "interleaved" layout, with the
+    frequencies of `base`, scaled by one of "none", "linear", "base", "parts" and "bands" (include/emb.h)."""
+
+    def __init__(self, rot: int, layout: str = "half", base: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original_len: float = 0.0, turns_low: float = 0.0, turns_high: float = 0.0,
+                 magnitude: float = 1.0):
+        self.handle = None
+        self.rot, self.layout, self.scaling = rot, layout, scaling
+        self.handle = emb_create_rotary(emb_rotary_desc(rot, ROT_LAYOUT[layout], ROT_SCALING[scaling], 0, base, factor,
+                                                        original_len, turns_low, turns_high, magnitude))
+
+    def close(self) -> None:
+        if self.handle:
+            emb_destroy_rotary(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class KVCache:
+    """A paged cache over the caller's tensors k and v, indexed [page, slot, head, dim] (any strides, the dim
+    elements of a head contiguous)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        self.handle = None
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must be [pages, slots, heads, dim] of one shape and type")
+        code = _dtype_code("the cache", k)
+        if not k.is_cuda or not v.is_cuda:
+            raise ValueError("the cache is not in device memory")
+        if k.shape[3] > 1 and (k.stride(3) != 1 or v.stride(3) != 1):
+            raise ValueError("the elements of one head must be contiguous")
+        self.k, self.v = k, v
+        self.pages, self.page, self.heads, self.dim = k.shape
+        self.error = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.handle = emb_create_kv(emb_kv_desc(k.data_ptr(), v.data_ptr(), *k.stride()[:3], *v.stride()[:3],
+                                                self.pages, self.page, self.heads, self.dim, code,
+                                                self.error.data_ptr()))
+
+    def close(self) -> None:
+        if self.handle:
+            emb_destroy_kv(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def check_error(self, stream=None) -> None:
+        """Waits for the stream; raises if a call met a bad page, length or offset since the last check."""
+        emb_check_kv_error(self.handle, stream)
 
 
 # ---- convenience: a context with the tensors behind it ---------------------

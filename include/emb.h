@@ -449,6 +449,199 @@ int emb_probe_reads(const void* buf, int64_t nrows, int64_t stride, int32_t xcd_
 int emb_probe_update(const float* src, int64_t nsrc, float* a, float* b, int64_t nrows, int32_t items,
                      void* hip_stream);
 
+/* ======================================================================
+ * Sequence operators: the attention of a ranking model over a user's
+ * history of items, next to the tables that its items are embedded from.
+ * Rotary positions, the per-head norm of queries and keys, a paged cache of
+ * keys and values, and the attention of many candidates over a shared
+ * history.
+ *
+ * Conventions, besides those at the top of this file
+ *   - "heads" operands are [tokens][heads][dim] in device memory, given as a
+ *     pointer, a token stride and a head stride (in elements); the dim
+ *     elements of one head are contiguous. q and k may be slices of one
+ *     fused projection.
+ *   - dtype (EMB_F32 | EMB_BF16 | EMB_F16) is the type of all heads operands
+ *     of a call. Arithmetic is fp32 and every result is rounded once, to
+ *     nearest even.
+ *   - No call allocates, synchronises or keeps anything between calls: all of
+ *     them can be captured into a graph.
+ *   - Device-side integers (positions, lengths, page tables) are not read by
+ *     the host. A value out of its range never leads to an access outside the
+ *     buffers; for the calls on a cache it raises the cache's error flag.
+ * ====================================================================== */
+
+/* ---- rotary positions --------------------------------------------------
+ * Of each head's dim elements the first `rot` are pairs (a_i, b_i), i < rot/2,
+ * turned by the angle position * f_i and scaled by `magnitude`:
+ *     a' = (a cos - b sin) * magnitude,  b' = (a sin + b cos) * magnitude;
+ * the elements from rot on are copied. EMB_ROT_HALF pairs element i with
+ * i + rot/2, EMB_ROT_INTERLEAVED 2i with 2i + 1. The frequencies f_i (radians
+ * per position) follow from `base` and `scaling`, with g_i = base^(-2i/rot):
+ *   EMB_ROT_NONE    f = g
+ *   EMB_ROT_LINEAR  f = g / factor
+ *   EMB_ROT_BASE    f = (base * factor^(rot/(rot-2)))^(-2i/rot)   (rot >= 4)
+ *   EMB_ROT_PARTS   f = g * keep + g / factor * (1 - keep), keep = ln(turns /
+ *                   turns_low) / ln(turns_high / turns_low) clamped to [0, 1],
+ *                   turns = original_len * g / (2 pi): pairs that turn often
+ *                   over the original length keep their frequency, slow ones
+ *                   are stretched
+ *   EMB_ROT_BANDS   the same with keep = (turns - turns_low) / (turns_high -
+ *                   turns_low)
+ * Angles are exact to 2^-31 of a turn for positions below 2^20 in magnitude
+ * (the frequency is held as a 64-bit fraction of a turn and multiplied by the
+ * position in integers; the error grows with the position from there). */
+#define EMB_ROT_HALF         0
+#define EMB_ROT_INTERLEAVED  1
+
+#define EMB_ROT_NONE    0
+#define EMB_ROT_LINEAR  1
+#define EMB_ROT_BASE    2
+#define EMB_ROT_PARTS   3
+#define EMB_ROT_BANDS   4
+
+#define EMB_MAX_ROT       256   /* largest rot */
+#define EMB_MAX_HEAD_DIM  1024  /* largest dim of a heads operand */
+
+typedef struct emb_rotary_desc {
+  int32_t rot;           /* even, 2..EMB_MAX_ROT */
+  int32_t layout;        /* EMB_ROT_HALF | EMB_ROT_INTERLEAVED */
+  int32_t scaling;       /* EMB_ROT_NONE .. EMB_ROT_BANDS */
+  int32_t reserved;      /* must be 0 */
+  double  base;          /* > 1 */
+  double  factor;        /* > 0; LINEAR, BASE, PARTS, BANDS */
+  double  original_len;  /* > 0; PARTS, BANDS */
+  double  turns_low;     /* > 0; PARTS, BANDS */
+  double  turns_high;    /* > turns_low; PARTS, BANDS */
+  double  magnitude;     /* finite, != 0 */
+} emb_rotary_desc;
+
+typedef struct emb_rotary emb_rotary;
+
+/* Computes the frequencies on the host. Touches no device. EMB_E_INVAL on a
+ * field out of its range. */
+int emb_create_rotary(const emb_rotary_desc* desc, emb_rotary** out);
+void emb_destroy_rotary(emb_rotary* rot);
+
+/* Turns the heads of q, and of k where k_heads > 0, by the position of their
+ * token: positions is [tokens] of itype, any sign. inverse != 0 applies the
+ * transposed map (angles negated, the same magnitude), which is the gradient.
+ * q_out may be q itself with the same strides, and k_out k; other overlaps are
+ * not allowed. rot <= dim <= EMB_MAX_HEAD_DIM. 16-byte aligned operands whose
+ * dim, rot and strides are multiples of 32 bytes (strides: 16) run at the
+ * memory's rate; any others go element by element. */
+int emb_rotary_apply(const emb_rotary* rot, const void* positions, int32_t itype, int64_t tokens, int32_t dtype,
+                     int32_t dim, const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                     int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t q_heads, const void* k,
+                     int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
+                     int64_t k_out_head_stride, int32_t k_heads, int32_t inverse, void* hip_stream);
+
+/* Norm of queries and keys for each head, with the rotation in the same pass:
+ *     y = rotate(x * r * w),  r = 1 / sqrt(mean over the head of x^2 + eps);
+ * wq and wk are fp32 [dim] (NULL: ones). Otherwise as emb_rotary_apply. */
+int emb_qk_norm_rotary(const emb_rotary* rot, const void* positions, int32_t itype, int64_t tokens, int32_t dtype,
+                       int32_t dim, const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                       int64_t q_out_token_stride, int64_t q_out_head_stride, int32_t q_heads, const void* k,
+                       int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
+                       int64_t k_out_head_stride, int32_t k_heads, const float* wq, const float* wk, float eps,
+                       void* hip_stream);
+
+/* Its gradient. q and k are the forward's inputs, dyq and dyk the gradients of
+ * its outputs, dq and dk receive those of its inputs, dwq and dwk (fp32 [dim],
+ * overwritten, NULL: not wanted) those of the weights, summed over tokens and
+ * heads in a fixed order (reruns are bit-identical). With u = rotate^T(dy),
+ * n = x r:  dx = r (u w - n mean(u w n)),  dw = sum of u n.
+ * dq may be dyq with the same strides, dk dyk. ws: device, 16-byte aligned, at
+ * least emb_qk_norm_rotary_workspace_bytes (0 on invalid arguments). */
+size_t emb_qk_norm_rotary_workspace_bytes(int64_t tokens, int32_t q_heads, int32_t k_heads, int32_t dim);
+int emb_qk_norm_rotary_backward(const emb_rotary* rot, const void* positions, int32_t itype, int64_t tokens,
+                                int32_t dtype, int32_t dim, const void* q, int64_t q_token_stride,
+                                int64_t q_head_stride, const void* dyq, int64_t dyq_token_stride,
+                                int64_t dyq_head_stride, void* dq, int64_t dq_token_stride, int64_t dq_head_stride,
+                                int32_t q_heads, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                                const void* dyk, int64_t dyk_token_stride, int64_t dyk_head_stride, void* dk,
+                                int64_t dk_token_stride, int64_t dk_head_stride, int32_t k_heads, const float* wq,
+                                const float* wk, float eps, void* ws, size_t ws_bytes, float* dwq, float* dwk,
+                                void* hip_stream);
+
+/* ---- a paged cache of keys and values ----------------------------------
+ * k and v hold `pages` pages of `page` slots of `heads` heads of `dim`
+ * elements; element (p, s, h, c) of k lies at k[p * k_page_stride + s *
+ * k_slot_stride + h * k_head_stride + c], v likewise. A sequence's page table
+ * row lists the pages of its slots 0.., page by page. */
+typedef struct emb_kv_desc {
+  void*   k;
+  void*   v;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;   /* elements, >= 0 */
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t pages;     /* 1 .. 2^31 - 1 */
+  int32_t page;      /* slots of a page, 1 .. 2^20 */
+  int32_t heads;     /* 1 .. 65535 */
+  int32_t dim;       /* 1 .. EMB_MAX_HEAD_DIM */
+  int32_t dtype;     /* EMB_F32 | EMB_BF16 | EMB_F16 */
+  int32_t* error;    /* device int32, set to 0 by the caller; NULL: no reports */
+} emb_kv_desc;
+
+typedef struct emb_kv emb_kv;
+
+/* Copies the descriptor. Touches no device state. */
+int emb_create_kv(const emb_kv_desc* desc, emb_kv** out);
+void emb_destroy_kv(emb_kv* kv);
+
+/* Synchronises the stream, reads and clears the cache's error flag:
+ * EMB_E_BOUNDS if a call met a page outside [0, pages) or a length that its
+ * page table does not hold, EMB_E_INVAL if it met offsets that break their
+ * contract, else EMB_OK (always without an error word). */
+int emb_check_kv_error(emb_kv* kv, void* hip_stream);
+
+/* Appends the keys and values of new tokens to their sequences' pages. k and v
+ * are heads operands; dtype, heads and dim have to be the cache's. Sequence b's new
+ * tokens are offsets[b] .. offsets[b+1] (int32 [seqs+1], offsets[0] = 0,
+ * non-decreasing, offsets[seqs] = tokens; NULL: token b is sequence b's only
+ * one, tokens = seqs), lens[b] (int32) its length with them, so its token j
+ * goes to slot lens[b] - (offsets[b+1] - offsets[b]) + j; table is int32
+ * [seqs][table_width]. Keys are normed per head first if norm != 0 (weights wk
+ * fp32 [dim] or NULL, eps; as emb_qk_norm_rotary) and turned if rot is not
+ * NULL, by positions[token] (of itype) or, where positions is NULL, by the
+ * slot. Values are copied. A token whose slot has no page (a negative slot,
+ * one beyond the table's width, a page outside [0, pages)) is not stored and
+ * raises the error flag. Two tokens of one call must not share a slot. */
+int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dtype, int32_t heads, int32_t dim,
+                  const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                  const int32_t* offsets, int32_t seqs, const int32_t* lens, const int32_t* table,
+                  int32_t table_width, const void* positions, int32_t itype, int32_t norm, const float* wk,
+                  float eps, void* hip_stream);
+
+/* Attention of queries over a prefix that their group shares and over their
+ * own sequence. q and out are heads operands [tokens][q_heads][dim];
+ * dtype and dim have to be the cache's, q_heads a multiple of the cache's heads (query head i
+ * reads cache head i / (q_heads / heads)). Sequence b's query tokens are
+ * offsets[b] .. offsets[b+1] (contract as emb_kv_append; NULL: one each), the
+ * last of its lens[b] own slots in table[b]: query j of n sees its own slots
+ * below lens[b] - n + j + 1. Group g holds sequences group_offsets[g] ..
+ * group_offsets[g+1] (int32 [groups+1], 0 to seqs, non-decreasing) and its
+ * prefix the first prefix_lens[g] slots of prefix_table[g] (int32
+ * [groups][prefix_width]); all queries of the group see all of it.
+ * groups = 0: no prefixes (the three pointers NULL).
+ *     out = sum_j softmax_j(scale * q . k_j) v_j,
+ *     lse = ln sum_j exp(scale * q . k_j)      (fp32 [tokens][q_heads], or NULL)
+ * A query that sees no slot gets zeros and -inf. Slots that a query does not
+ * see have no influence on it, whatever they hold.
+ * EMB_BF16 / EMB_F16 caches with dim 64, 96 or 128; k, v, q and out 16-byte
+ * aligned and their strides multiples of 16 bytes; EMB_E_INVAL otherwise
+ * (EMB_E_DTYPE for an fp32 cache). Softmax statistics and sums are fp32; the
+ * probabilities are rounded to the cache's type for the matrix product.
+ * ws: device, 16-byte aligned, at least
+ * emb_prefix_attention_workspace_bytes (0 on invalid arguments). */
+size_t emb_prefix_attention_workspace_bytes(const emb_kv* kv, int64_t tokens, int32_t q_heads, int32_t groups,
+                                            int32_t prefix_width, int32_t table_width);
+int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim, const void* q,
+                         int64_t q_token_stride, int64_t q_head_stride, void* out, int64_t out_token_stride, int64_t out_head_stride, int32_t q_heads, float scale,
+                         const int32_t* offsets, int32_t seqs, const int32_t* lens, const int32_t* table,
+                         int32_t table_width, const int32_t* group_offsets, int32_t groups,
+                         const int32_t* prefix_lens, const int32_t* prefix_table, int32_t prefix_width, void* ws,
+                         size_t ws_bytes, float* lse, void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
