@@ -97,14 +97,14 @@ FastDiv fast_div(uint32_t d) {
   return FastDiv{(uint32_t)((1ull << (31 + s)) / d + 1), 31 + s, d};
 }
 
-// Blocks of the gradient kernel. Its 256 threads are groups that take one
-// head each; a block count that is a multiple of q_heads + k_heads keeps every
-// group on one head, so that it sums one weight's gradient only. Four blocks
-// per CU hide the memory's latency; fewer where there is less work than that.
+// Blocks of the gradient kernel. Its groups of lanes take 4 heads each; a
+// block count that is a multiple of the head groups keeps every group on one
+// of them, so that it sums one weight's gradient only. Four blocks per CU hide
+// the memory's latency; fewer where there is less work than that.
 int norm_rotary_back_blocks(long long tokens, int hq, int hk, int dim) {
-  const long long heads = (long long)hq + hk;
+  const long long heads = (hq + 3) / 4 + (hk + 3) / 4;
   if (heads == 0 || tokens == 0) return 0;
-  const long long work = (tokens * heads + 15) / 16;  // at least 16 heads for each block
+  const long long work = (tokens * heads + 7) / 8;
   const long long n = std::min<long long>(work, 1024);
   return (int)((n + heads - 1) / heads * heads);
 }

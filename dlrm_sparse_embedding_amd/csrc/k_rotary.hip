@@ -261,6 +261,241 @@ __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part,
   }
 }
 
+// ---- 16-byte units ---------------------------------------------------------------
+
+// Sum over the lanes of a group of G neighbours (a power of two, at most 32):
+// lane exchanges inside rows of 16 are operand modifiers, not LDS traffic.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float near_sum(float x, int G) {
+  if (G > 1) x += dpp<0xB1>(x);   // swap neighbours
+  if (G > 2) x += dpp<0x4E>(x);   // swap pairs
+  if (G > 4) x += dpp<0x141>(x);  // mirror 8 lanes: quads are uniform by now
+  if (G > 8) x += dpp<0x140>(x);  // mirror 16 lanes
+  if (G > 16) x += __shfl_xor(x, 16, 64);
+  return x;
+}
+
+template <int DT>
+constexpr int kV = DT == EMB_F32 ? 4 : 8;  // elements of 16 bytes
+
+// A lane's unit of 2 V elements.
+template <int DT, int LAYOUT>
+struct Unit {
+  static constexpr int V = kV<DT>;
+  int e0, e1;     // its two runs of V elements
+  bool turns;     // it holds pairs
+  float c[V], s[V];
+
+  __device__ __forceinline__ void place(int u, const RotTable& rot) {
+    turns = 2 * V * u < rot.rot;
+    e0 = 2 * V * u;
+    e1 = e0 + V;
+    if (LAYOUT == EMB_ROT_HALF && turns) {
+      e0 = V * u;
+      e1 = rot.rot / 2 + V * u;
+    }
+  }
+  __device__ __forceinline__ void angles(int u, const RotTable& rot, long long pos, float sign) {
+    if (!turns) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      sincos_turn(rot.turn[V * u + j], pos, rot.mag, &c[j], &s[j]);
+      s[j] *= sign;
+    }
+  }
+  // x: the unit's elements, run 0 then run 1
+  __device__ __forceinline__ void turn(float* x) const {
+    if (!turns) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int ia = LAYOUT == EMB_ROT_HALF ? j : 2 * j, ib = LAYOUT == EMB_ROT_HALF ? V + j : 2 * j + 1;
+      const float a = x[ia], b = x[ib];
+      x[ia] = a * c[j] - b * s[j];
+      x[ib] = a * s[j] + b * c[j];
+    }
+  }
+};
+
+template <int DT>
+__device__ __forceinline__ const u4* at16(const void* p, long long i) {
+  return reinterpret_cast<const u4*>(reinterpret_cast<const typename Elem<DT>::T*>(p) + i);
+}
+template <int DT>
+__device__ __forceinline__ void put16(const void* p, long long i, const float* x) {
+  *reinterpret_cast<u4*>(reinterpret_cast<typename Elem<DT>::T*>(const_cast<void*>(p)) + i) = narrow<DT>(x);
+}
+
+// The unit's part of a weight (ones where it is null).
+template <int V>
+__device__ __forceinline__ void load_w(const float* w, int e0, int e1, float* out) {
+#pragma unroll
+  for (int j = 0; j < 2 * V; ++j) out[j] = 1.f;
+  if (!w) return;
+#pragma unroll
+  for (int j = 0; j < V; j += 4) {
+    load4<EMB_F32>(w + e0 + j, out + j);
+    load4<EMB_F32>(w + e1 + j, out + V + j);
+  }
+}
+
+// The lanes of a call: groups of G lanes (units of them busy), one group for
+// HPT heads of one token, so that one set of angles serves them all; queries
+// and keys are never in one group, so a group has one weight.
+struct VecShape {
+  int G, units;
+  int gq, gk;      // head groups of the queries (values, in the append: of the keys) and of the keys (values)
+  FastDiv by_g;    // by gq + gk
+  long long items; // tokens * (gq + gk) < 2^31
+};
+
+template <int DT, int LAYOUT, int NORM, int HPT>
+__global__ __launch_bounds__(256) void k_norm_rotary_vec(NormRotaryArgs a, VecShape sh, RotTable rot) {
+  constexpr int V = kV<DT>;
+  const int u = threadIdx.x & (sh.G - 1);
+  const int per = 256 / sh.G;
+  const bool busy = u < sh.units;
+  Unit<DT, LAYOUT> un;
+  un.place(u, rot);
+  for (long long item = (long long)blockIdx.x * per + threadIdx.x / sh.G; item < sh.items;
+       item += (long long)gridDim.x * per) {
+    const int t = (int)(((uint64_t)(uint32_t)item * sh.by_g.mul) >> sh.by_g.shift);
+    const int g = (int)item - t * (int)sh.by_g.d;
+    const bool isq = g < sh.gq;
+    const Heads& in = isq ? a.q : a.k;
+    const Heads& out = isq ? a.qo : a.ko;
+    const int h0 = (isq ? g : g - sh.gq) * HPT;
+    u4 lo[HPT], hi[HPT];
+    if (busy) {
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        const int h = min(h0 + i, in.n - 1);
+        lo[i] = *at16<DT>(in.p, t * in.ts + h * in.hs + un.e0);
+        hi[i] = *at16<DT>(in.p, t * in.ts + h * in.hs + un.e1);
+      }
+      un.angles(u, rot, position(a.positions, a.itype, t), a.inverse ? -1.f : 1.f);
+    }
+    float w[2 * V];
+    if (NORM) {
+      if (busy) load_w<V>(isq ? a.wq : a.wk, un.e0, un.e1, w);
+    }
+#pragma unroll
+    for (int i = 0; i < HPT; ++i) {
+      float x[2 * V];
+      if (busy) {
+        widen<DT>(lo[i], x);
+        widen<DT>(hi[i], x + V);
+      }
+      if (NORM) {
+        float ss = 0.f;
+        if (busy) {
+#pragma unroll
+          for (int j = 0; j < 2 * V; ++j) ss += x[j] * x[j];
+        }
+        const float r = 1.f / sqrtf(near_sum(ss, sh.G) / (float)a.dim + a.eps);
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) x[j] *= r * w[j];
+      }
+      if (busy && h0 + i < in.n) {
+        const long long yi = t * out.ts + (h0 + i) * out.hs;
+        if (!NORM && !un.turns) {  // a copy, whatever the bits
+          *const_cast<u4*>(at16<DT>(out.p, yi + un.e0)) = lo[i];
+          *const_cast<u4*>(at16<DT>(out.p, yi + un.e1)) = hi[i];
+        } else {
+          un.turn(x);
+          put16<DT>(out.p, yi + un.e0, x);
+          put16<DT>(out.p, yi + un.e1, x + V);
+        }
+      }
+    }
+  }
+}
+
+// Gradient. The grid's groups are a multiple of the head groups, so a group
+// stays on one head group and sums one weight's gradient in its registers over
+// all its tokens; the block's groups are joined through LDS in their order.
+constexpr int kBackHeads = 4;
+
+template <int DT, int LAYOUT>
+__global__ __launch_bounds__(256) void k_norm_rotary_back_vec(NormRotaryBackArgs a, VecShape sh, RotTable rot) {
+  constexpr int V = kV<DT>;
+  __shared__ float s_dw[256 * 2 * V];
+  const int u = threadIdx.x & (sh.G - 1);
+  const int per = 256 / sh.G;
+  const bool busy = u < sh.units;
+  const int HG = sh.gq + sh.gk;
+  Unit<DT, LAYOUT> un;
+  un.place(u, rot);
+  const long long first = (long long)blockIdx.x * per + threadIdx.x / sh.G;
+  const int g = (int)(first % HG);
+  const bool isq = g < sh.gq;
+  const Heads& in = isq ? a.q : a.k;
+  const Heads& dyh = isq ? a.dyq : a.dyk;
+  const Heads& dxh = isq ? a.dq : a.dk;
+  const int h0 = (isq ? g : g - sh.gq) * kBackHeads;
+  float w[2 * V], dw[2 * V];
+#pragma unroll
+  for (int j = 0; j < 2 * V; ++j) dw[j] = 0.f;
+  if (busy) load_w<V>(isq ? a.wq : a.wk, un.e0, un.e1, w);
+  for (long long t = first / HG; t < a.tokens; t += (long long)gridDim.x * per / HG) {
+    if (busy) un.angles(u, rot, position(a.positions, a.itype, t), -1.f);
+#pragma unroll
+    for (int i = 0; i < kBackHeads; ++i) {
+      const int h = h0 + i;
+      if (h >= in.n) break;  // the same for all lanes of the group
+      float x[2 * V], d[2 * V], ss = 0.f, dot = 0.f;
+      if (busy) {
+        const long long xi = t * in.ts + h * in.hs, yi = t * dyh.ts + h * dyh.hs;
+        widen<DT>(*at16<DT>(in.p, xi + un.e0), x);
+        widen<DT>(*at16<DT>(in.p, xi + un.e1), x + V);
+        widen<DT>(*at16<DT>(dyh.p, yi + un.e0), d);
+        widen<DT>(*at16<DT>(dyh.p, yi + un.e1), d + V);
+        un.turn(d);
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) {
+          ss += x[j] * x[j];
+          dot += d[j] * w[j] * x[j];
+        }
+      }
+      const float r = 1.f / sqrtf(near_sum(ss, sh.G) / (float)a.dim + a.eps);
+      const float mean = near_sum(dot, sh.G) * r / (float)a.dim;
+      if (busy) {
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) {
+          const float n = x[j] * r;
+          dw[j] += d[j] * n;
+          d[j] = r * (d[j] * w[j] - n * mean);
+        }
+        const long long oi = t * dxh.ts + h * dxh.hs;
+        put16<DT>(dxh.p, oi + un.e0, d);
+        put16<DT>(dxh.p, oi + un.e1, d + V);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2 * V; ++j) s_dw[threadIdx.x * 2 * V + j] = busy ? dw[j] : 0.f;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.dim; i += 256) {
+    const bool wantq = i < a.dim;
+    const int e = wantq ? i : i - a.dim;
+    // unit and place of element e
+    int uu = e / (2 * V), j = e % (2 * V);
+    if (LAYOUT == EMB_ROT_HALF && e < rot.rot) {
+      const int half = rot.rot / 2, ee = e < half ? e : e - half;
+      uu = ee / V;
+      j = ee % V + (e < half ? 0 : V);
+    }
+    float sum = 0.f;
+    for (int q = 0; q < per; ++q) {
+      const int gg = (int)(((long long)blockIdx.x * per + q) % HG);
+      if ((gg < sh.gq) == wantq) sum += s_dw[(q * sh.G + uu) * 2 * V + j];
+    }
+    a.part[(long long)blockIdx.x * 2 * a.dim + i] = sum;
+  }
+}
+
 // ---- the append -----------------------------------------------------------------
 
 // The sequence of token t: the last b with offsets[b] <= t.
@@ -332,9 +567,156 @@ __global__ __launch_bounds__(256) void k_append_any(AppendArgs a, RotTable rot) 
   }
 }
 
+template <int DT, int LAYOUT, int HPT>
+__global__ __launch_bounds__(256) void k_append_vec(AppendArgs a, VecShape sh, RotTable rot) {
+  constexpr int V = kV<DT>;
+  const KvView& kv = a.kv;
+  const int u = threadIdx.x & (sh.G - 1);
+  const int per = 256 / sh.G;
+  const bool busy = u < sh.units;
+  Unit<DT, LAYOUT> un;
+  un.place(u, rot);
+  for (long long item = (long long)blockIdx.x * per + threadIdx.x / sh.G; item < sh.items;
+       item += (long long)gridDim.x * per) {
+    const int t = (int)(((uint64_t)(uint32_t)item * sh.by_g.mul) >> sh.by_g.shift);
+    const int g = (int)item - t * (int)sh.by_g.d;
+    const bool isk = g < sh.gq;
+    const Heads& in = isk ? a.k : a.v;
+    const int h0 = (isk ? g : g - sh.gq) * HPT;
+    u4 lo[HPT], hi[HPT];
+    if (busy) {
+#pragma unroll
+      for (int i = 0; i < HPT; ++i) {
+        const int h = min(h0 + i, in.n - 1);
+        lo[i] = *at16<DT>(in.p, t * in.ts + h * in.hs + un.e0);
+        hi[i] = *at16<DT>(in.p, t * in.ts + h * in.hs + un.e1);
+      }
+    }
+    int page, in_page, slot;
+    if (!place(a, t, &page, &in_page, &slot)) continue;  // the same for all lanes of the group
+    char* out = isk ? kv.k : kv.v;
+    const long long row = isk ? page * kv.kps + in_page * kv.kss : page * kv.vps + in_page * kv.vss;
+    const long long hs = isk ? kv.khs : kv.vhs;
+    float w[2 * V];
+    if (isk && busy) {
+      un.angles(u, rot, a.positions ? position(a.positions, a.itype, t) : (long long)slot, 1.f);
+      if (a.norm) load_w<V>(a.wk, un.e0, un.e1, w);
+    }
+#pragma unroll
+    for (int i = 0; i < HPT; ++i) {
+      const bool store = busy && h0 + i < in.n;
+      const long long yi = row + (h0 + i) * hs;
+      if (!isk || (!a.norm && !un.turns)) {
+        if (store) {
+          *const_cast<u4*>(at16<DT>(out, yi + un.e0)) = lo[i];
+          *const_cast<u4*>(at16<DT>(out, yi + un.e1)) = hi[i];
+        }
+        if (!isk || !a.norm) continue;
+      }
+      float x[2 * V];
+      if (busy) {
+        widen<DT>(lo[i], x);
+        widen<DT>(hi[i], x + V);
+      }
+      if (a.norm) {
+        float ss = 0.f;
+        if (busy) {
+#pragma unroll
+          for (int j = 0; j < 2 * V; ++j) ss += x[j] * x[j];
+        }
+        const float r = 1.f / sqrtf(near_sum(ss, sh.G) / (float)kv.dim + a.eps);
+#pragma unroll
+        for (int j = 0; j < 2 * V; ++j) x[j] *= r * w[j];
+      }
+      if (store) {
+        un.turn(x);
+        put16<DT>(out, yi + un.e0, x);
+        put16<DT>(out, yi + un.e1, x + V);
+      }
+    }
+  }
+}
+
+// Whether 16-byte units fit an operand.
+bool fits(const Heads& h, int dtype) {
+  const int V = dtype == EMB_F32 ? 4 : 8;
+  return h.n == 0 || (reinterpret_cast<uintptr_t>(h.p) % 16 == 0 && h.ts % V == 0 && h.hs % V == 0);
+}
+
+// Units of the calls over dim elements with this rotation; G = 0 where they do not fit.
+VecShape vec_shape(int dtype, int dim, const RotTable& rot, long long tokens, int nq, int nk, int hpt) {
+  VecShape sh{};
+  const int V2 = dtype == EMB_F32 ? 8 : 16;
+  sh.gq = (nq + hpt - 1) / hpt;
+  sh.gk = (nk + hpt - 1) / hpt;
+  sh.items = tokens * (sh.gq + sh.gk);
+  if (dim % V2 != 0 || rot.rot % V2 != 0 || dim / V2 > 32 || sh.items >= (1ll << 31)) return sh;
+  sh.units = dim / V2;
+  sh.G = 1;
+  while (sh.G < sh.units) sh.G *= 2;
+  sh.by_g = fast_div((uint32_t)(sh.gq + sh.gk));
+  return sh;
+}
+
+unsigned vec_grid(const VecShape& sh) {
+  const int per = 256 / sh.G;
+  return (unsigned)std::min<long long>((sh.items + per - 1) / per, 1 << 20);
+}
+
+// Heads for each group of lanes. Four share their angles and keep 128 bytes a
+// lane in flight; with little work one head each spreads it over the chip.
+int heads_per_group(long long tokens, int heads, int units) {
+  return tokens * heads * units >= (1ll << 20) ? 4 : 1;
+}
+
+template <int DT, int LAYOUT, int NORM>
+void launch_vec(const NormRotaryArgs& a, const VecShape& sh, int hpt, const RotTable& rot, hipStream_t st) {
+  if (hpt == 4) k_norm_rotary_vec<DT, LAYOUT, NORM, 4><<<vec_grid(sh), 256, 0, st>>>(a, sh, rot);
+  else k_norm_rotary_vec<DT, LAYOUT, NORM, 1><<<vec_grid(sh), 256, 0, st>>>(a, sh, rot);
+}
+
+template <int DT>
+void launch_vec_t(const NormRotaryArgs& a, const VecShape& sh, int hpt, const RotTable& rot, hipStream_t st) {
+  if (rot.layout == EMB_ROT_HALF) {
+    if (a.norm) launch_vec<DT, EMB_ROT_HALF, 1>(a, sh, hpt, rot, st);
+    else launch_vec<DT, EMB_ROT_HALF, 0>(a, sh, hpt, rot, st);
+  } else {
+    if (a.norm) launch_vec<DT, EMB_ROT_INTERLEAVED, 1>(a, sh, hpt, rot, st);
+    else launch_vec<DT, EMB_ROT_INTERLEAVED, 0>(a, sh, hpt, rot, st);
+  }
+}
+
+template <int DT>
+void launch_back_vec(const NormRotaryBackArgs& a, int blocks, const VecShape& sh, const RotTable& rot, hipStream_t st) {
+  if (rot.layout == EMB_ROT_HALF) k_norm_rotary_back_vec<DT, EMB_ROT_HALF><<<blocks, 256, 0, st>>>(a, sh, rot);
+  else k_norm_rotary_back_vec<DT, EMB_ROT_INTERLEAVED><<<blocks, 256, 0, st>>>(a, sh, rot);
+}
+
+template <int DT, int LAYOUT>
+void launch_append_vec(const AppendArgs& a, const VecShape& sh, int hpt, const RotTable& rot, hipStream_t st) {
+  if (hpt == 4) k_append_vec<DT, LAYOUT, 4><<<vec_grid(sh), 256, 0, st>>>(a, sh, rot);
+  else k_append_vec<DT, LAYOUT, 1><<<vec_grid(sh), 256, 0, st>>>(a, sh, rot);
+}
+
+template <int DT>
+void launch_append_vec_t(const AppendArgs& a, const VecShape& sh, int hpt, const RotTable& rot, hipStream_t st) {
+  if (rot.layout == EMB_ROT_HALF) launch_append_vec<DT, EMB_ROT_HALF>(a, sh, hpt, rot, st);
+  else launch_append_vec<DT, EMB_ROT_INTERLEAVED>(a, sh, hpt, rot, st);
+}
+
 }  // namespace
 
 hipError_t launch_norm_rotary(const NormRotaryArgs& a, const RotTable& rot, hipStream_t st) {
+  if (fits(a.q, a.dtype) && fits(a.qo, a.dtype) && fits(a.k, a.dtype) && fits(a.ko, a.dtype)) {
+    const int hpt = heads_per_group(a.tokens, a.q.n + a.k.n, a.dim / (a.dtype == EMB_F32 ? 8 : 16));
+    const VecShape sh = vec_shape(a.dtype, a.dim, rot, a.tokens, a.q.n, a.k.n, hpt);
+    if (sh.G > 0) {
+      if (a.dtype == EMB_F32) launch_vec_t<EMB_F32>(a, sh, hpt, rot, st);
+      else if (a.dtype == EMB_BF16) launch_vec_t<EMB_BF16>(a, sh, hpt, rot, st);
+      else launch_vec_t<EMB_F16>(a, sh, hpt, rot, st);
+      return hipGetLastError();
+    }
+  }
   const long long items = a.tokens * (a.q.n + a.k.n);
   const unsigned grid = (unsigned)std::min<long long>((items + 3) / 4, 1 << 20);
   if (a.dtype == EMB_F32) k_norm_rotary_any<EMB_F32><<<grid, 256, 0, st>>>(a, rot);
@@ -345,7 +727,15 @@ hipError_t launch_norm_rotary(const NormRotaryArgs& a, const RotTable& rot, hipS
 
 hipError_t launch_norm_rotary_back(const NormRotaryBackArgs& a, const RotTable& rot, hipStream_t st) {
   const int blocks = norm_rotary_back_blocks(a.tokens, a.q.n, a.k.n, a.dim);
-  if (blocks > 0) {
+  const bool fit = fits(a.q, a.dtype) && fits(a.dyq, a.dtype) && fits(a.dq, a.dtype) && fits(a.k, a.dtype) &&
+                   fits(a.dyk, a.dtype) && fits(a.dk, a.dtype);
+  const VecShape sh = vec_shape(a.dtype, a.dim, rot, a.tokens, a.q.n, a.k.n, kBackHeads);
+  if (blocks > 0 && fit && sh.G > 0) {
+    if (a.dtype == EMB_F32) launch_back_vec<EMB_F32>(a, blocks, sh, rot, st);
+    else if (a.dtype == EMB_BF16) launch_back_vec<EMB_BF16>(a, blocks, sh, rot, st);
+    else launch_back_vec<EMB_F16>(a, blocks, sh, rot, st);
+    if (hipError_t e = hipGetLastError()) return e;
+  } else if (blocks > 0) {
     const size_t lds = 8 * sizeof(float) * a.dim;
     if (a.dtype == EMB_F32) k_norm_rotary_back_any<EMB_F32><<<blocks, 256, lds, st>>>(a, rot);
     else if (a.dtype == EMB_BF16) k_norm_rotary_back_any<EMB_BF16><<<blocks, 256, lds, st>>>(a, rot);
@@ -357,6 +747,20 @@ hipError_t launch_norm_rotary_back(const NormRotaryBackArgs& a, const RotTable& 
 }
 
 hipError_t launch_kv_append(const AppendArgs& a, const RotTable& rot, hipStream_t st) {
+  const KvView& c = a.kv;
+  const Heads ck{c.k, c.kss, c.khs, c.heads}, cv{c.v, c.vss, c.vhs, c.heads};
+  const int V = c.dtype == EMB_F32 ? 4 : 8;
+  if (fits(a.k, c.dtype) && fits(a.v, c.dtype) && fits(ck, c.dtype) && fits(cv, c.dtype) && c.kps % V == 0 &&
+      c.vps % V == 0) {
+    const int hpt = heads_per_group(a.tokens, 2 * c.heads, c.dim / (2 * V));
+    const VecShape sh = vec_shape(c.dtype, c.dim, rot, a.tokens, c.heads, c.heads, hpt);
+    if (sh.G > 0) {
+      if (c.dtype == EMB_F32) launch_append_vec_t<EMB_F32>(a, sh, hpt, rot, st);
+      else if (c.dtype == EMB_BF16) launch_append_vec_t<EMB_BF16>(a, sh, hpt, rot, st);
+      else launch_append_vec_t<EMB_F16>(a, sh, hpt, rot, st);
+      return hipGetLastError();
+    }
+  }
   const long long items = a.tokens * 2 * a.kv.heads;
   const unsigned grid = (unsigned)std::min<long long>((items + 3) / 4, 1 << 20);
   if (a.kv.dtype == EMB_F32) k_append_any<EMB_F32><<<grid, 256, 0, st>>>(a, rot);
