@@ -121,11 +121,16 @@ PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, long lon
   const long long pcap = groups > 0 ? (long long)pwidth * kv.page : 0;
   const long long ocap = (long long)width * kv.page;
   if (pcap > 0) {
-    const long long tiles = std::max<long long>(groups, (tokens * m + 31) / 32);
+    // Rows of one group and cache head, on average; the wide tiles fetch 4 or 8
+    // slots of a page at a time.
+    p.wide = tokens * m > 64ll * groups && kv.page % 8 == 0;
+    const int rows = p.wide ? 128 : 32;
+    const long long tiles = std::max<long long>(groups, (tokens * m + rows - 1) / rows);
     const long long want = (512 + tiles * kv.heads - 1) / (tiles * kv.heads);
     p.nps = (int)std::max<long long>(1, std::min<long long>({want, (pcap + 255) / 256, 32}));
-    p.prefix_tiles = groups + tokens * m / 32;
+    p.prefix_tiles = groups + tokens * m / rows;
     p.prefix_blocks = p.prefix_tiles * kv.heads * p.nps;
+    if (p.wide) p.prefix_blocks = (p.prefix_blocks + 7) / 8 * 8;
   }
   const long long waves = (tokens * m + 31) / 32 * kv.heads;
   const long long want = (2048 + waves - 1) / waves;

@@ -24,6 +24,7 @@
 // the unrounded ones). They are scaled by 2^8, so that fp16 keeps its full
 // precision down to 2^-22 of a row's largest.
 #include <algorithm>
+#include <cmath>
 
 #include "emb_device.h"
 #include "seq_internal.h"
@@ -42,7 +43,8 @@ typedef float fl2 __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 
-constexpr float kShift = 8.f;    // probabilities carry this many powers of two
+constexpr float kShift = 8.f;  // probabilities carry this many powers of two
+constexpr float kSlack = 7.f;  // and this many more before the reference moves
 constexpr float kNegInf = -__builtin_inff();
 
 template <int DT>
@@ -60,12 +62,28 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, hf2));
 }
 
-// Exchange with the lane that holds the other 16 slots of the same row.
-__device__ __forceinline__ float other_half(float x) { return __shfl_xor(x, 32, 64); }
+// A row's two lanes (l and l + 32) joined.
+__device__ __forceinline__ void halves(float x, float* lo, float* hi) {
+  typedef unsigned u2v __attribute__((ext_vector_type(2)));
+  const u2v r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  *lo = __uint_as_float(r.x);
+  *hi = __uint_as_float(r.y);
+}
+__device__ __forceinline__ float both_halves_max(float x) {
+  float lo, hi;
+  halves(x, &lo, &hi);
+  return fmaxf(lo, hi);
+}
+__device__ __forceinline__ float both_halves_sum(float x) {
+  float lo, hi;
+  halves(x, &lo, &hi);
+  return lo + hi;
+}
 
 struct PrefixDev {
   PrefixArgs a;
-  float scale2;  // scale * log2(e)
+  float scale2;  // |scale| * log2(e), never 0
+  uint32_t q_sign;  // sign bits of two elements where the scale is negative
   int m;         // query heads of a cache head
   FastDiv by_m;
   int nps, nos;
@@ -141,7 +159,11 @@ __device__ __forceinline__ void load_q(const PrefixDev& p, const Rows& it, Wave<
   const int head = it.h * p.m + rr - j * p.m;
   const short* src = reinterpret_cast<const short*>(p.a.q.p) + (long long)(it.t0 + j) * p.a.q.ts + head * p.a.q.hs;
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) w.q[s] = *reinterpret_cast<const s8v*>(src + 16 * s + 8 * (lane >> 5));
+  for (int s = 0; s < D / 16; ++s) {
+    u4 x = *reinterpret_cast<const u4*>(src + 16 * s + 8 * (lane >> 5));
+    x ^= p.q_sign;  // a negative scale is taken into q, so that maxima stay maxima
+    w.q[s] = __builtin_bit_cast(s8v, x);
+  }
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) w.o[d] = f16v{};
   w.mx = kNegInf;
@@ -180,26 +202,20 @@ __device__ __forceinline__ s8v read_vt(const short* v, int kk, int d0) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Turns a tile's scores (raw products) into probabilities packed for the V
-// product, updating the running maximum and sum and rescaling the outputs.
-// Slots at and beyond `seen` (the lane's own limit) get none; `masked` is
-// uniform and says whether any lane's limit cuts the tile.
-template <int DT, int D>
-__device__ __forceinline__ void softmax_tile(const PrefixDev& p, Wave<DT, D>& w, f16v s, int slot0, int seen,
-                                             bool masked, s8v* prob) {
-  const int lane = threadIdx.x & 63;
+// Turns the scores (raw products) of N tiles of 32 slots into probabilities
+// packed for the V product, updating the running maximum and sum. Masked
+// scores are -infinity already. The outputs are rescaled only where a maximum
+// has grown by more than kSlack since the reference was set: any reference
+// gives the same quotient, and the slack keeps the probabilities below 2^15.
+template <int DT, int D, int N>
+__device__ __forceinline__ void softmax_tiles(const PrefixDev& p, Wave<DT, D>& w, f16v (&s)[N], s8v (&prob)[2 * N]) {
+  float top = s[0][0];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) s[i] *= p.scale2;
-  if (masked) {
+  for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (slot0 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4 >= seen) s[i] = kNegInf;
-  }
-  float top = s[0];
-#pragma unroll
-  for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-  top = fmaxf(top, other_half(top));
-  if (__ballot(top > w.mx)) {
+    for (int i = n == 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
+  top = both_halves_max(top) * p.scale2;
+  if (__ballot(top > w.mx + kSlack)) {
     const float mx = fmaxf(w.mx, top);
     const float keep = mx == kNegInf ? 1.f : __builtin_amdgcn_exp2f(w.mx - mx);
     w.mx = mx;
@@ -209,23 +225,35 @@ __device__ __forceinline__ void softmax_tile(const PrefixDev& p, Wave<DT, D>& w,
 #pragma unroll
       for (int i = 0; i < 16; ++i) w.o[d][i] *= keep;
   }
-  const float ref = (w.mx == kNegInf ? 0.f : w.mx) - kShift;
+  const float add = kShift - (w.mx == kNegInf ? 0.f : w.mx);
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(s[i] - ref);
-    sum += s[i];
-  }
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], p.scale2, add));
+      sum += s[n][i];
+    }
   w.sum += sum;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
+  for (int k = 0; k < 2 * N; ++k) {
+    const f16v& x = s[k / 2];
+    const int i = 8 * (k % 2);
     u4 b;
-    b.x = pack2<DT>(s[8 * k], s[8 * k + 1]);
-    b.y = pack2<DT>(s[8 * k + 2], s[8 * k + 3]);
-    b.z = pack2<DT>(s[8 * k + 4], s[8 * k + 5]);
-    b.w = pack2<DT>(s[8 * k + 6], s[8 * k + 7]);
+    b.x = pack2<DT>(x[i], x[i + 1]);
+    b.y = pack2<DT>(x[i + 2], x[i + 3]);
+    b.z = pack2<DT>(x[i + 4], x[i + 5]);
+    b.w = pack2<DT>(x[i + 6], x[i + 7]);
     prob[k] = __builtin_bit_cast(s8v, b);
   }
+}
+
+// Clears the scores of a tile's slots at and beyond `seen` (the lane's own limit).
+__device__ __forceinline__ void mask_tile(f16v& s, int slot0, int seen) {
+  const int h4 = 4 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (slot0 + 8 * (i / 4) + h4 + i % 4 >= seen) s[i] = kNegInf;
 }
 
 // One wave over slots k0, k0 + step, .. below k1 in tiles of 32, the keys
@@ -256,16 +284,17 @@ __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages,
       vr[i] = *reinterpret_cast<const s8v*>(reinterpret_cast<const short*>(kv.v) + pg * kv.vps + sl * kv.vss +
                                             h * kv.vhs + 8 * (piece % (D / 8)));
     }
-    f16v s = {};
+    f16v s[1] = {};
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) s = mfma<DT>(kf[i], w.q[i], s);
+    for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(kf[i], w.q[i], s[0]);
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
       const int piece = i * 64 + lane;
       *reinterpret_cast<s8v*>(v + piece / (D / 8) * (D + kVPad) + 8 * (piece % (D / 8))) = vr[i];
     }
     s8v prob[2];
-    softmax_tile<DT, D>(p, w, s, k, seen, k + 32 > lim_lo, prob);
+    if (k + 32 > lim_lo) mask_tile(s[0], k, seen);
+    softmax_tiles<DT, D, 1>(p, w, s, prob);
     if (k + 32 <= lim_lo || lim_lo == lim_hi) {
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -301,7 +330,7 @@ template <int DT, int D>
 __device__ __forceinline__ void store_part(const PrefixDev& p, const Rows& it, Wave<DT, D>& w, int part) {
   const int lane = threadIdx.x & 63;
   const int row = it.r0 + (lane & 31);
-  const float total = w.sum + other_half(w.sum);
+  const float total = both_halves_sum(w.sum);
   if (row >= it.rows) return;
   const int j = div_by(p.by_m, row);
   const int head = it.h * p.m + row - j * p.m;
@@ -319,12 +348,89 @@ __device__ __forceinline__ void store_part(const PrefixDev& p, const Rows& it, W
           f4{w.o[d][4 * i] * inv, w.o[d][4 * i + 1] * inv, w.o[d][4 * i + 2] * inv, w.o[d][4 * i + 3] * inv};
 }
 
-// Prefix: a block takes one tile of 32 rows, a cache head and a part of the
-// prefix; its four waves take every fourth tile of slots and are joined in
-// LDS. Own sequence: each wave for itself takes a tile of rows, a cache head
-// and a part of the sequence.
+// A prefix block's work: tile `tile` of the groups' tiles of `rows` rows, and a
+// part of the prefix. False where there is none.
+struct PrefixItem {
+  Rows it;
+  const int* pages;
+  int k0, k1;
+};
+__device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows, PrefixItem* w, int* part) {
+  // the tile fastest (neighbours read the same slots), then the part, then the cache head
+  const int tile = id % p.prefix_tiles;
+  id /= p.prefix_tiles;
+  *part = id % p.nps;
+  const int h = id / p.nps;
+  if (h >= p.a.kv.heads) return false;  // the grid is a multiple of 8
+  // tile i of the group whose tiles start at g + (its first row) / rows
+  const int g = wave_find(p.a.groups, tile, [&](int i) { return i + group_token(p, i) * p.m / rows; });
+  const int t0 = group_token(p, g), t1 = group_token(p, g + 1);
+  w->it = Rows{t0, (tile - (g + t0 * p.m / rows)) * rows, (t1 - t0) * p.m, h};
+  if (tile == 0 && *part == 0 && h == 0 && threadIdx.x == 0 &&
+      (p.a.group_offsets[0] != 0 || p.a.group_offsets[p.a.groups] != p.a.seqs))
+    flag(p, kKvBadOffsets);
+  if (w->it.r0 < 0 || w->it.r0 >= w->it.rows) return false;  // the bound counts more tiles than there are
+  int len = p.a.prefix_lens[g];
+  const long long cap = (long long)p.a.pwidth * p.a.kv.page;
+  if (len < 0 || len > cap) {
+    if (threadIdx.x == 0) flag(p, kKvBadPage);
+    len = len < 0 ? 0 : (int)cap;
+  }
+  const int chunk = max(256, ((len + p.nps - 1) / p.nps + 127) & ~127);
+  w->k0 = (int)min((long long)*part * chunk, (long long)len);
+  w->k1 = min(w->k0 + chunk, len);
+  w->pages = p.a.prefix_table + (long long)g * p.a.pwidth;
+  return true;
+}
+
+// Own sequences: each wave of block `block` for itself takes a tile of rows, a
+// cache head and a part of the sequence; part fastest, then the tile, then the
+// cache head.
 template <int DT, int D>
-__global__ __launch_bounds__(256) void k_attend(PrefixDev p) {
+__device__ void own_part(const PrefixDev& p, int block, short* v) {
+  const int lane = threadIdx.x & 63;
+  int id = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = id % p.nos;
+  id /= p.nos;
+  const int tile = id % p.own_tiles;
+  const int h = id / p.own_tiles;
+  if (h >= p.a.kv.heads) return;
+  const int b = wave_find(p.a.seqs, tile, [&](int i) { return i + first_token(p, i) / p.own_tq; });
+  const int t0 = first_token(p, b), t1 = first_token(p, b + 1);
+  const int j0 = (tile - (b + t0 / p.own_tq)) * p.own_tq;  // first token of the tile, counted from t0
+  if (tile == 0 && part == 0 && h == 0 && lane == 0 && p.a.offsets &&
+      (p.a.offsets[0] != 0 || p.a.offsets[p.a.seqs] != p.a.tokens))
+    flag(p, kKvBadOffsets);
+  const int n = t1 - t0;
+  if (j0 < 0 || j0 >= n) return;
+  int len = p.a.lens[b];
+  const long long cap = (long long)p.a.width * p.a.kv.page;
+  if (len < 0 || len > cap) {
+    if (lane == 0) flag(p, kKvBadPage);
+    len = len < 0 ? 0 : (int)cap;
+  }
+  const int j1 = min(j0 + p.own_tq, n);
+  const int lim_lo = max(len - n + j0 + 1, 0), lim_hi = max(len - n + j1, 0);
+  const int chunk = max(128, ((lim_hi + p.nos - 1) / p.nos + 31) & ~31);
+  const int k0 = part * chunk;
+  // more than 32 query heads of one cache head: a token takes several tiles of rows
+  for (int r0 = j0 * p.m; r0 < j1 * p.m; r0 += 32) {
+    const Rows it{t0, r0, j1 * p.m, h};
+    Wave<DT, D> w;
+    load_q<DT, D>(p, it, w);
+    const int j = div_by(p.by_m, min(r0 + (lane & 31), it.rows - 1));
+    const int seen = max(len - n + j + 1, 0);
+    if (k0 < lim_hi)
+      wave_slots<DT, D>(p, w, p.a.table + (long long)b * p.a.width, h, k0, min(k0 + chunk, lim_hi), 32, seen, lim_lo,
+                        lim_hi, v);
+    store_part<DT, D>(p, it, w, p.nps + part);
+  }
+}
+
+// Few rows: a block takes one tile of 32 rows, a cache head and a part of the
+// prefix; its four waves take every fourth tile of slots and are joined in LDS.
+template <int DT, int D>
+__global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
   constexpr int OS = D + 4;  // row stride of the joined outputs (floats): rows start 4 banks apart
   constexpr size_t kV = 4 * v_tile_elems<D>() * sizeof(short), kO = (2 * 32 * OS + 4 * 64) * sizeof(float);
   __shared__ __attribute__((aligned(16))) char smem[kV > kO ? kV : kO];
@@ -332,30 +438,12 @@ __global__ __launch_bounds__(256) void k_attend(PrefixDev p) {
   short* v = reinterpret_cast<short*>(smem) + wave * v_tile_elems<D>();
   Wave<DT, D> w;
   if ((int)blockIdx.x < p.prefix_blocks) {
-    // part of the prefix fastest, then the tile, then the cache head
-    int id = blockIdx.x;
-    const int part = id % p.nps;
-    id /= p.nps;
-    const int tile = id % p.prefix_tiles;
-    const int h = id / p.prefix_tiles;
-    // tile i of the group whose tiles start at g + (its first row) / 32
-    const int g = wave_find(p.a.groups, tile, [&](int i) { return i + group_token(p, i) * p.m / 32; });
-    const int t0 = group_token(p, g), t1 = group_token(p, g + 1);
-    Rows it{t0, (tile - (g + t0 * p.m / 32)) * 32, (t1 - t0) * p.m, h};
-    if (tile == 0 && part == 0 && h == 0 && threadIdx.x == 0 &&
-        (p.a.group_offsets[0] != 0 || p.a.group_offsets[p.a.groups] != p.a.seqs))
-      flag(p, kKvBadOffsets);
-    if (it.r0 < 0 || it.r0 >= it.rows) return;  // the bound counts more tiles than there are
-    int len = p.a.prefix_lens[g];
-    const long long cap = (long long)p.a.pwidth * p.a.kv.page;
-    if (len < 0 || len > cap) {
-      if (threadIdx.x == 0) flag(p, kKvBadPage);
-      len = len < 0 ? 0 : (int)cap;
-    }
-    const int chunk = max(256, ((len + p.nps - 1) / p.nps + 127) & ~127);
-    const int k0 = min((long long)part * chunk, (long long)len), k1 = min(k0 + chunk, len);
+    PrefixItem x;
+    int part;
+    if (!prefix_item(p, blockIdx.x, 32, &x, &part)) return;
+    const Rows it = x.it;
     load_q<DT, D>(p, it, w);
-    wave_slots<DT, D>(p, w, p.a.prefix_table + (long long)g * p.a.pwidth, h, k0 + 32 * wave, k1, 128, k1, k1, k1, v);
+    wave_slots<DT, D>(p, w, x.pages, it.h, x.k0 + 32 * wave, x.k1, 128, x.k1, x.k1, x.k1, v);
     // join: waves 2 and 3 into 0 and 1, then 1 into 0
     float* so = reinterpret_cast<float*>(smem);
     float* sm = so + 2 * 32 * OS;
@@ -394,42 +482,137 @@ __global__ __launch_bounds__(256) void k_attend(PrefixDev p) {
     if (wave == 0) store_part<DT, D>(p, it, w, part);
     return;
   }
-  // own sequences: part fastest, then the tile, then the cache head
-  int id = ((int)blockIdx.x - p.prefix_blocks) * 4 + wave;
-  const int part = id % p.nos;
-  id /= p.nos;
-  const int tile = id % p.own_tiles;
-  const int h = id / p.own_tiles;
-  if (h >= p.a.kv.heads) return;
-  const int b = wave_find(p.a.seqs, tile, [&](int i) { return i + first_token(p, i) / p.own_tq; });
-  const int t0 = first_token(p, b), t1 = first_token(p, b + 1);
-  const int j0 = (tile - (b + t0 / p.own_tq)) * p.own_tq;  // first token of the tile, counted from t0
-  if (tile == 0 && part == 0 && h == 0 && lane == 0 && p.a.offsets &&
-      (p.a.offsets[0] != 0 || p.a.offsets[p.a.seqs] != p.a.tokens))
-    flag(p, kKvBadOffsets);
-  const int n = t1 - t0;
-  if (j0 < 0 || j0 >= n) return;
-  int len = p.a.lens[b];
-  const long long cap = (long long)p.a.width * p.a.kv.page;
-  if (len < 0 || len > cap) {
-    if (lane == 0) flag(p, kKvBadPage);
-    len = len < 0 ? 0 : (int)cap;
+  own_part<DT, D>(p, blockIdx.x - p.prefix_blocks, v);
+}
+
+// Many rows: a block takes NW * 32 rows of one cache head and a part of the
+// prefix, each wave 32 rows; tiles of 64 slots go through LDS for all of them.
+// While one tile is worked on, the next is on its way to registers; it is put
+// into the other half of LDS before the barrier that ends the step.
+//
+// A wave fetches whole slots' rows, kGroup at a time, so that with pages of a
+// multiple of kGroup slots the page is the same for the wave and its address
+// is scalar arithmetic.
+constexpr int kTile = 64;
+constexpr int kKPad = 8;  // elements: 8 rows of K start 4 banks apart, so 16-byte reads of 8 rows meet all banks once
+
+template <int D>
+constexpr int group_slots() {
+  return D == 64 ? 8 : 4;
+}
+
+typedef __attribute__((address_space(4))) const int const_int;
+
+template <int DT, int D, int NW>
+struct Stage {
+  static constexpr int kGroup = group_slots<D>();
+  static constexpr int kN = kTile / (NW * kGroup);  // groups of a wave
+  u4 k[kN], v[kN];
+};
+
+template <int DT, int D, int NW>
+__device__ __forceinline__ void fetch_tile(const PrefixDev& p, const const_int* pages, int h, int slot0, int k1,
+                                           Stage<DT, D, NW>& st) {
+  using S = Stage<DT, D, NW>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const KvView& kv = p.a.kv;
+  const int r = lane / (D / 8), c = lane % (D / 8);
+  const long long klane = (long long)r * kv.kss + 8 * c, vlane = (long long)r * kv.vss + 8 * c;
+#pragma unroll
+  for (int i = 0; i < S::kN; ++i) {
+    // a group past the end fetches the last one again
+    const int slot = min(slot0 + (i * NW + wave) * S::kGroup, (k1 - 1) / S::kGroup * S::kGroup);
+    const int col = div_by(kv.by_page, slot);
+    int pg = pages[col];
+    if (pg < 0 || pg >= kv.pages) {
+      if (lane == 0) flag(p, kKvBadPage);
+      pg = 0;
+    }
+    const long long in = slot - col * kv.page;
+    const short* kb = reinterpret_cast<const short*>(kv.k) + (pg * kv.kps + in * kv.kss + h * kv.khs);
+    const short* vb = reinterpret_cast<const short*>(kv.v) + (pg * kv.vps + in * kv.vss + h * kv.vhs);
+    if (r < S::kGroup) {
+      st.k[i] = *reinterpret_cast<const u4*>(kb + klane);
+      st.v[i] = *reinterpret_cast<const u4*>(vb + vlane);
+    }
   }
-  const int j1 = min(j0 + p.own_tq, n);
-  const int lim_lo = max(len - n + j0 + 1, 0), lim_hi = max(len - n + j1, 0);
-  const int chunk = max(128, ((lim_hi + p.nos - 1) / p.nos + 31) & ~31);
-  const int k0 = part * chunk;
-  // more than 32 query heads of one cache head: a token takes several tiles of rows
-  for (int r0 = j0 * p.m; r0 < j1 * p.m; r0 += 32) {
-    Rows it{t0, r0, j1 * p.m, h};
-    load_q<DT, D>(p, it, w);
-    const int j = div_by(p.by_m, min(r0 + (lane & 31), it.rows - 1));
-    const int seen = max(len - n + j + 1, 0);
-    if (k0 < lim_hi)
-      wave_slots<DT, D>(p, w, p.a.table + (long long)b * p.a.width, h, k0, min(k0 + chunk, lim_hi), 32, seen, lim_lo,
-                        lim_hi, v);
-    store_part<DT, D>(p, it, w, p.nps + part);
+}
+
+template <int DT, int D, int NW>
+__device__ __forceinline__ void put_tile(const Stage<DT, D, NW>& st, short* k, short* v, int slot0, int k1) {
+  using S = Stage<DT, D, NW>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane / (D / 8), c = lane % (D / 8);
+#pragma unroll
+  for (int i = 0; i < S::kN; ++i) {
+    const int row = (i * NW + wave) * S::kGroup + r;
+    if (r < S::kGroup) {
+      *reinterpret_cast<u4*>(k + row * (D + kKPad) + 8 * c) = st.k[i];
+      // values behind the end are cleared: a probability of zero must not meet an infinity
+      *reinterpret_cast<u4*>(v + row * (D + kVPad) + 8 * c) = slot0 + row < k1 ? st.v[i] : u4{0, 0, 0, 0};
+    }
   }
+}
+
+template <int DT, int D, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
+  constexpr int kKTile = kTile * (D + kKPad), kVTile = kTile * (D + kVPad);
+  constexpr int kWide = 2 * (kKTile + kVTile), kOwn = NW * v_tile_elems<D>();
+  __shared__ __attribute__((aligned(16))) short smem[kWide > kOwn ? kWide : kOwn];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if ((int)blockIdx.x >= p.prefix_blocks) {
+    own_part<DT, D>(p, blockIdx.x - p.prefix_blocks, smem + wave * v_tile_elems<D>());
+    return;
+  }
+  PrefixItem x;
+  int part;
+  // blocks are dealt to the 8 XCDs in turn: neighbours in the work's order,
+  // which read the same part of the prefix, go to one XCD and its L2
+  if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
+  const const_int* pages = (const const_int*)(uintptr_t)x.pages;
+  Rows it = x.it;
+  it.r0 += 32 * wave;
+  const bool live = it.r0 < it.rows;  // waves without rows only fetch
+  Wave<DT, D> w;
+  load_q<DT, D>(p, it, w);
+  Stage<DT, D, NW> st;
+  if (x.k0 < x.k1) {
+    fetch_tile<DT, D, NW>(p, pages, it.h, x.k0, x.k1, st);
+    put_tile<DT, D, NW>(st, smem, smem + kKTile, x.k0, x.k1);
+    __syncthreads();
+  }
+  int buf = 0;
+  for (int k = x.k0; k < x.k1; k += kTile, buf ^= 1) {
+    const short* ks = smem + buf * (kKTile + kVTile);
+    const short* vs = ks + kKTile;
+    const bool more = k + kTile < x.k1;
+    if (more) fetch_tile<DT, D, NW>(p, pages, it.h, k + kTile, x.k1, st);
+    if (live) {
+      f16v s[2] = {};
+      const short* kr = ks + (lane & 31) * (D + kKPad) + 8 * (lane >> 5);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+          s[n] = mfma<DT>(*reinterpret_cast<const s8v*>(kr + 32 * n * (D + kKPad) + 16 * i), w.q[i], s[n]);
+      if (k + kTile > x.k1) {
+        mask_tile(s[0], k, x.k1);
+        mask_tile(s[1], k + 32, x.k1);
+      }
+      s8v prob[4];
+      softmax_tiles<DT, D, 2>(p, w, s, prob);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) w.o[d] = mfma<DT>(read_vt<D>(vs, 16 * kk, 32 * d), prob[kk], w.o[d]);
+    }
+    if (more) {
+      short* to = smem + (buf ^ 1) * (kKTile + kVTile);
+      put_tile<DT, D, NW>(st, to, to + kKTile, k + kTile, x.k1);
+    }
+    __syncthreads();
+  }
+  if (live) store_part<DT, D>(p, it, w, part);
 }
 
 // Joins the parts of each (token, query head): 32 lanes, 4 columns each.
@@ -472,8 +655,9 @@ __global__ __launch_bounds__(256) void k_join(PrefixDev p) {
 }
 
 template <int DT, int D>
-hipError_t launch(const PrefixDev& p, int blocks, hipStream_t st) {
-  k_attend<DT, D><<<blocks, 256, 0, st>>>(p);
+hipError_t launch(const PrefixDev& p, int blocks, bool wide, hipStream_t st) {
+  if (wide) k_attend_wide<DT, D, 4><<<blocks, 256, 0, st>>>(p);
+  else k_attend<DT, D><<<blocks, 256, 0, st>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
   const long long rows = (long long)p.a.tokens * p.a.q_heads;
   k_join<DT, D><<<(unsigned)std::min<long long>((rows + 7) / 8, 1 << 20), 256, 0, st>>>(p);
@@ -485,7 +669,10 @@ hipError_t launch(const PrefixDev& p, int blocks, hipStream_t st) {
 hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& plan, char* ws, hipStream_t st) {
   PrefixDev p{};
   p.a = a;
-  p.scale2 = a.scale * 1.4426950408889634f;
+  // a scale of 0 would turn a masked -infinity into NaN; 1e-37 scales every
+  // finite product of 16-bit operands to less than half a step of 1
+  p.scale2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-37f);
+  p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
   p.m = a.q_heads / a.kv.heads;
   p.by_m = fast_div((uint32_t)p.m);
   p.nps = plan.nps;
@@ -499,9 +686,9 @@ hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& plan, 
   const int blocks = (int)(plan.prefix_blocks + plan.own_blocks);
   const bool bf = a.kv.dtype == EMB_BF16;
   switch (a.kv.dim) {
-    case 64: return bf ? launch<EMB_BF16, 64>(p, blocks, st) : launch<EMB_F16, 64>(p, blocks, st);
-    case 96: return bf ? launch<EMB_BF16, 96>(p, blocks, st) : launch<EMB_F16, 96>(p, blocks, st);
-    default: return bf ? launch<EMB_BF16, 128>(p, blocks, st) : launch<EMB_F16, 128>(p, blocks, st);
+    case 64: return bf ? launch<EMB_BF16, 64>(p, blocks, plan.wide, st) : launch<EMB_F16, 64>(p, blocks, plan.wide, st);
+    case 96: return bf ? launch<EMB_BF16, 96>(p, blocks, plan.wide, st) : launch<EMB_F16, 96>(p, blocks, plan.wide, st);
+    default: return bf ? launch<EMB_BF16, 128>(p, blocks, plan.wide, st) : launch<EMB_F16, 128>(p, blocks, plan.wide, st);
   }
 }
 

@@ -124,6 +124,7 @@ struct PrefixArgs {
 // of group (sequence) i are numbered from i + floor(first row / R).
 struct PrefixPlan {
   int nps, nos;
+  bool wide;   // prefix tiles of 128 rows that share their keys in LDS, else 32
   int own_tq;  // query tokens of an own tile
   long long prefix_tiles, prefix_blocks, own_tiles, own_blocks;
   size_t o_off;     // partial outputs fp32 [nps + nos][tokens][q_heads][dim]
