@@ -202,19 +202,23 @@ __device__ __forceinline__ s8v read_vt(const short* v, int kk, int d0) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Turns the scores (raw products) of N tiles of 32 slots into probabilities
-// packed for the V product, updating the running maximum and sum. Masked
-// scores are -infinity already. The outputs are rescaled only where a maximum
-// has grown by more than kSlack since the reference was set: any reference
-// gives the same quotient, and the slack keeps the probabilities below 2^15.
-template <int DT, int D, int N>
-__device__ __forceinline__ void softmax_tiles(const PrefixDev& p, Wave<DT, D>& w, f16v (&s)[N], s8v (&prob)[2 * N]) {
+template <int N>
+__device__ __forceinline__ float top_of(const f16v (&s)[N]) {
   float top = s[0][0];
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int i = n == 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
-  top = both_halves_max(top) * p.scale2;
+  return top;
+}
+
+// Takes N tiles' scores (raw products) into the running maximum. The outputs
+// are rescaled only where a maximum has grown by more than kSlack since the
+// reference was set: any reference gives the same quotient, and the slack
+// keeps the probabilities below 2^15.
+template <int DT, int D, int N>
+__device__ __forceinline__ void refer(const PrefixDev& p, Wave<DT, D>& w, const f16v (&s)[N]) {
+  const float top = both_halves_max(top_of(s)) * p.scale2;
   if (__ballot(top > w.mx + kSlack)) {
     const float mx = fmaxf(w.mx, top);
     const float keep = mx == kNegInf ? 1.f : __builtin_amdgcn_exp2f(w.mx - mx);
@@ -225,27 +229,31 @@ __device__ __forceinline__ void softmax_tiles(const PrefixDev& p, Wave<DT, D>& w
 #pragma unroll
       for (int i = 0; i < 16; ++i) w.o[d][i] *= keep;
   }
+}
+
+// Probabilities of N tiles of 32 slots, packed for the V product, and their
+// sum. Masked scores are -infinity already.
+template <int DT, int D, int N>
+__device__ __forceinline__ void probabilities(const PrefixDev& p, Wave<DT, D>& w, f16v (&s)[N], s8v (&prob)[2 * N]) {
   const float add = kShift - (w.mx == kNegInf ? 0.f : w.mx);
   float sum = 0.f;
 #pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[n][i] = __builtin_amdgcn_exp2f(fmaf(s[n][i], p.scale2, add));
-      sum += s[n][i];
-    }
-  w.sum += sum;
-#pragma unroll
   for (int k = 0; k < 2 * N; ++k) {
-    const f16v& x = s[k / 2];
-    const int i = 8 * (k % 2);
+    f16v& x = s[k / 2];
+    const int i0 = 8 * (k % 2);
+#pragma unroll
+    for (int i = i0; i < i0 + 8; ++i) {
+      x[i] = __builtin_amdgcn_exp2f(fmaf(x[i], p.scale2, add));
+      sum += x[i];
+    }
     u4 b;
-    b.x = pack2<DT>(x[i], x[i + 1]);
-    b.y = pack2<DT>(x[i + 2], x[i + 3]);
-    b.z = pack2<DT>(x[i + 4], x[i + 5]);
-    b.w = pack2<DT>(x[i + 6], x[i + 7]);
+    b.x = pack2<DT>(x[i0], x[i0 + 1]);
+    b.y = pack2<DT>(x[i0 + 2], x[i0 + 3]);
+    b.z = pack2<DT>(x[i0 + 4], x[i0 + 5]);
+    b.w = pack2<DT>(x[i0 + 6], x[i0 + 7]);
     prob[k] = __builtin_bit_cast(s8v, b);
   }
+  w.sum += sum;
 }
 
 // Clears the scores of a tile's slots at and beyond `seen` (the lane's own limit).
@@ -294,7 +302,8 @@ __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages,
     }
     s8v prob[2];
     if (k + 32 > lim_lo) mask_tile(s[0], k, seen);
-    softmax_tiles<DT, D, 1>(p, w, s, prob);
+    refer<DT, D, 1>(p, w, s);
+    probabilities<DT, D, 1>(p, w, s, prob);
     if (k + 32 <= lim_lo || lim_lo == lim_hi) {
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
@@ -487,79 +496,128 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
 
 // Many rows: a block takes NW * 32 rows of one cache head and a part of the
 // prefix, each wave 32 rows; tiles of 64 slots go through LDS for all of them.
-// While one tile is worked on, the next is on its way to registers; it is put
-// into the other half of LDS before the barrier that ends the step.
 //
-// A wave fetches whole slots' rows, kGroup at a time, so that with pages of a
-// multiple of kGroup slots the page is the same for the wave and its address
-// is scalar arithmetic.
+// Pipeline. While 32 slots' scores are turned into probabilities, the matrix
+// units already make the next 32 slots' scores; the product with V follows. K
+// therefore runs 32 slots ahead of V: a step works on V of slots k .. k + 63 and
+// K of k + 32 .. k + 95. The next step's tiles are on their way meanwhile,
+// straight from memory into the other half of LDS, with no registers in
+// between: one barrier a step, where they have to have landed.
+//
+// LDS. A fetch writes 16 bytes a lane in lane order, so rows lie without
+// padding and the lane picks which 16 bytes of its row it brings: piece c of
+// row r lies at c ^ swizzle(r), chosen so that the 8 rows that a K read and the
+// 4 rows that a transposed V read meet at once lie in different banks.
+//
+// A wave fetches whole slots' rows, kGroup at a time; with pages of a multiple
+// of kGroup slots the page is the same for the wave and the address scalar.
 constexpr int kTile = 64;
-constexpr int kKPad = 8;  // elements: 8 rows of K start 4 banks apart, so 16-byte reads of 8 rows meet all banks once
 
 template <int D>
 constexpr int group_slots() {
   return D == 64 ? 8 : 4;
 }
-
-typedef __attribute__((address_space(4))) const int const_int;
-
-template <int DT, int D, int NW>
-struct Stage {
-  static constexpr int kGroup = group_slots<D>();
-  static constexpr int kN = kTile / (NW * kGroup);  // groups of a wave
-  u4 k[kN], v[kN];
-};
-
-template <int DT, int D, int NW>
-__device__ __forceinline__ void fetch_tile(const PrefixDev& p, const const_int* pages, int h, int slot0, int k1,
-                                           Stage<DT, D, NW>& st) {
-  using S = Stage<DT, D, NW>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const KvView& kv = p.a.kv;
-  const int r = lane / (D / 8), c = lane % (D / 8);
-  const long long klane = (long long)r * kv.kss + 8 * c, vlane = (long long)r * kv.vss + 8 * c;
-#pragma unroll
-  for (int i = 0; i < S::kN; ++i) {
-    // a group past the end fetches the last one again
-    const int slot = min(slot0 + (i * NW + wave) * S::kGroup, (k1 - 1) / S::kGroup * S::kGroup);
-    const int col = div_by(kv.by_page, slot);
-    int pg = pages[col];
-    if (pg < 0 || pg >= kv.pages) {
-      if (lane == 0) flag(p, kKvBadPage);
-      pg = 0;
-    }
-    const long long in = slot - col * kv.page;
-    const short* kb = reinterpret_cast<const short*>(kv.k) + (pg * kv.kps + in * kv.kss + h * kv.khs);
-    const short* vb = reinterpret_cast<const short*>(kv.v) + (pg * kv.vps + in * kv.vss + h * kv.vhs);
-    if (r < S::kGroup) {
-      st.k[i] = *reinterpret_cast<const u4*>(kb + klane);
-      st.v[i] = *reinterpret_cast<const u4*>(vb + vlane);
-    }
-  }
+template <int D>
+__device__ __forceinline__ int swizzle_k(int r) {
+  return D == 96 ? (r >> 1) & 3 : r & 7;
+}
+template <int D>
+__device__ __forceinline__ int swizzle_v(int r) {
+  return D == 96 ? r & 2 : 2 * (r & 3);
 }
 
-template <int DT, int D, int NW>
-__device__ __forceinline__ void put_tile(const Stage<DT, D, NW>& st, short* k, short* v, int slot0, int k1) {
-  using S = Stage<DT, D, NW>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int r = lane / (D / 8), c = lane % (D / 8);
+typedef __attribute__((address_space(4))) const int const_int;
+typedef __attribute__((address_space(3))) short lds_short;
+
+// 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
+// The compiler does not see the transfer: the caller waits (wait_fetch) and
+// passes a barrier before anyone reads.
+__device__ __forceinline__ void fetch16(const void* base, uint32_t off, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(at), "v"(off), "s"(base)
+               : "memory");
+}
+__device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <int D, int NW>
+struct Fetch {
+  static constexpr int kGroup = group_slots<D>();
+  static constexpr int kN = kTile / (NW * kGroup);  // groups of a wave in a tile
+  uint32_t koff, voff;  // the lane's byte offset in a group's rows
+  bool on;              // the lane has a piece
+  int wave;
+
+  __device__ __forceinline__ void init(const PrefixDev& p) {
+    const int lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane / (D / 8), c = lane % (D / 8);
+    const int row = wave * kGroup + r;  // NW * kGroup is a multiple of 8: every group of the wave swizzles alike
+    on = r < kGroup;
+    koff = 2 * (uint32_t)(r * p.a.kv.kss + 8 * (c ^ swizzle_k<D>(row)));
+    voff = 2 * (uint32_t)(r * p.a.kv.vss + 8 * (c ^ swizzle_v<D>(row)));
+  }
+  // First slot of group i of the tile at slot0; a group past the end repeats the last one.
+  __device__ __forceinline__ int slot(int slot0, int k1, int i) const {
+    return min(slot0 + (i * NW + wave) * kGroup, (k1 - 1) / kGroup * kGroup);
+  }
+  __device__ __forceinline__ void pages(const PrefixDev& p, const const_int* table, int slot0, int k1,
+                                        int (&pg)[kN]) const {
 #pragma unroll
-  for (int i = 0; i < S::kN; ++i) {
-    const int row = (i * NW + wave) * S::kGroup + r;
-    if (r < S::kGroup) {
-      *reinterpret_cast<u4*>(k + row * (D + kKPad) + 8 * c) = st.k[i];
-      // values behind the end are cleared: a probability of zero must not meet an infinity
-      *reinterpret_cast<u4*>(v + row * (D + kVPad) + 8 * c) = slot0 + row < k1 ? st.v[i] : u4{0, 0, 0, 0};
+    for (int i = 0; i < kN; ++i) pg[i] = table[div_by(p.a.kv.by_page, slot(slot0, k1, i))];
+  }
+  __device__ __forceinline__ void tile(const PrefixDev& p, const char* base, long long ps, long long ss, uint32_t off,
+                                       int slot0, int k1, const int (&pg)[kN], uint32_t at) const {
+    const KvView& kv = p.a.kv;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int s = slot(slot0, k1, i);
+      int page = pg[i];
+      if (page < 0 || page >= kv.pages) {
+        flag(p, kKvBadPage);
+        page = 0;
+      }
+      const char* from = base + 2 * (page * ps + (s - div_by(kv.by_page, s) * kv.page) * ss);
+      if (on) fetch16(from, off, at + (i * NW + wave) * kGroup * 2 * D);
     }
   }
+};
+
+// The scores of 32 slots: K (rows of LDS at k) by the wave's queries.
+template <int DT, int D>
+__device__ __forceinline__ void scores(const Wave<DT, D>& w, const short* k, f16v (&s)[1]) {
+  const int lane = threadIdx.x & 63, r = lane & 31;
+  const int sw = swizzle_k<D>(r) ^ (lane >> 5);
+  s[0] = f16v{};
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i)
+    s[0] = mfma<DT>(*reinterpret_cast<const s8v*>(k + r * D + 8 * ((2 * i) ^ sw)), w.q[i], s[0]);
+}
+
+// The outputs' product with V (rows of LDS at v) of 32 slots.
+template <int DT, int D>
+__device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, const s8v (&prob)[2]) {
+  const int lane = threadIdx.x & 63, q = lane & 15;
+  const int r = 4 * (lane >> 5) + (q >> 2);
+  const int c = 2 * ((lane >> 4) & 1) + ((q & 3) >> 1), sw = swizzle_v<D>(r);  // the same for r + 8
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) {
+      const short* at = v + (16 * kk + r) * D + 8 * ((4 * d + c) ^ sw) + 4 * (q & 1);
+      const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
+      const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D));
+      w.o[d] = mfma<DT>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), prob[kk], w.o[d]);
+    }
 }
 
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
-  constexpr int kKTile = kTile * (D + kKPad), kVTile = kTile * (D + kVPad);
-  constexpr int kWide = 2 * (kKTile + kVTile), kOwn = NW * v_tile_elems<D>();
-  __shared__ __attribute__((aligned(16))) short smem[kWide > kOwn ? kWide : kOwn];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  using F = Fetch<D, NW>;
+  constexpr int kRows = kTile * D;  // elements of a tile
+  constexpr int kWide = 4 * kRows, kOwn = NW * v_tile_elems<D>();
+  __shared__ __attribute__((aligned(1024))) short smem[kWide > kOwn ? kWide : kOwn];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if ((int)blockIdx.x >= p.prefix_blocks) {
     own_part<DT, D>(p, blockIdx.x - p.prefix_blocks, smem + wave * v_tile_elems<D>());
     return;
@@ -569,48 +627,69 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   // blocks are dealt to the 8 XCDs in turn: neighbours in the work's order,
   // which read the same part of the prefix, go to one XCD and its L2
   if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
-  const const_int* pages = (const const_int*)(uintptr_t)x.pages;
+  const const_int* table = (const_int*)(uintptr_t)x.pages;
+  const KvView& kv = p.a.kv;
+  const int k1 = x.k1;
   Rows it = x.it;
+  const char* kbase = kv.k + 2 * it.h * kv.khs;
+  const char* vbase = kv.v + 2 * it.h * kv.vhs;
   it.r0 += 32 * wave;
   const bool live = it.r0 < it.rows;  // waves without rows only fetch
   Wave<DT, D> w;
   load_q<DT, D>(p, it, w);
-  Stage<DT, D, NW> st;
-  if (x.k0 < x.k1) {
-    fetch_tile<DT, D, NW>(p, pages, it.h, x.k0, x.k1, st);
-    put_tile<DT, D, NW>(st, smem, smem + kKTile, x.k0, x.k1);
+  if (x.k0 < k1) {
+    F f;
+    f.init(p);
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_short*)smem;
+    // K tiles at 0 and 1, V tiles at 2 and 3
+    auto at = [&](int i) { return lds + 2 * kRows * i; };
+    int pg[F::kN], pn[F::kN];  // pages of a tile of V and of K
+    f.pages(p, table, x.k0, k1, pg);
+    f.pages(p, table, x.k0 + 32, k1, pn);
+    f.tile(p, kbase, kv.kps, kv.kss, f.koff, x.k0, k1, pg, at(1));
+    f.tile(p, vbase, kv.vps, kv.vss, f.voff, x.k0, k1, pg, at(2));
+    f.tile(p, kbase, kv.kps, kv.kss, f.koff, x.k0 + 32, k1, pn, at(0));
+    f.pages(p, table, x.k0 + kTile, k1, pg);
+    f.pages(p, table, x.k0 + kTile + 32, k1, pn);
+    wait_fetch();
     __syncthreads();
-  }
-  int buf = 0;
-  for (int k = x.k0; k < x.k1; k += kTile, buf ^= 1) {
-    const short* ks = smem + buf * (kKTile + kVTile);
-    const short* vs = ks + kKTile;
-    const bool more = k + kTile < x.k1;
-    if (more) fetch_tile<DT, D, NW>(p, pages, it.h, k + kTile, x.k1, st);
+    f16v s[1], t[1];
     if (live) {
-      f16v s[2] = {};
-      const short* kr = ks + (lane & 31) * (D + kKPad) + 8 * (lane >> 5);
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-          s[n] = mfma<DT>(*reinterpret_cast<const s8v*>(kr + 32 * n * (D + kKPad) + 16 * i), w.q[i], s[n]);
-      if (k + kTile > x.k1) {
-        mask_tile(s[0], k, x.k1);
-        mask_tile(s[1], k + 32, x.k1);
-      }
-      s8v prob[4];
-      softmax_tiles<DT, D, 2>(p, w, s, prob);
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) w.o[d] = mfma<DT>(read_vt<D>(vs, 16 * kk, 32 * d), prob[kk], w.o[d]);
-    }
-    if (more) {
-      short* to = smem + (buf ^ 1) * (kKTile + kVTile);
-      put_tile<DT, D, NW>(st, to, to + kKTile, k + kTile, x.k1);
+      scores<DT, D>(w, smem + kRows, s);
+      if (x.k0 + 32 > k1) mask_tile(s[0], x.k0, k1);
     }
     __syncthreads();
+    int b = 0;
+    for (int k = x.k0; k < k1; k += kTile, b ^= 1) {
+      const short* ks = smem + b * kRows;
+      short* vs = smem + (2 + b) * kRows;
+      if (k + kTile < k1) {
+        f.tile(p, kbase, kv.kps, kv.kss, f.koff, k + kTile + 32, k1, pn, at(1 - b));
+        f.tile(p, vbase, kv.vps, kv.vss, f.voff, k + kTile, k1, pg, at(3 - b));
+        f.pages(p, table, k + 2 * kTile, k1, pg);
+        f.pages(p, table, k + 2 * kTile + 32, k1, pn);
+      } else if (k + kTile > k1) {
+        // values behind the end are cleared: a probability of zero must not meet an infinity
+        for (int i = threadIdx.x; i < (k + kTile - k1) * (D / 8); i += NW * 64)
+          *reinterpret_cast<u4*>(vs + (k1 - k) * D + 8 * i) = u4{0, 0, 0, 0};
+        __syncthreads();
+      }
+      if (live) {
+        s8v prob[2];
+        refer<DT, D, 1>(p, w, s);
+        scores<DT, D>(w, ks, t);
+        probabilities<DT, D, 1>(p, w, s, prob);
+        times_v<DT, D>(w, vs, prob);
+        if (k + 64 > k1) mask_tile(t[0], k + 32, k1);
+        refer<DT, D, 1>(p, w, t);
+        scores<DT, D>(w, ks + 32 * D, s);
+        probabilities<DT, D, 1>(p, w, t, prob);
+        times_v<DT, D>(w, vs + 32 * D, prob);
+        if (k + 96 > k1) mask_tile(s[0], k + 64, k1);
+      }
+      wait_fetch();
+      __syncthreads();
+    }
   }
   if (live) store_part<DT, D>(p, it, w, part);
 }
