@@ -183,12 +183,17 @@ __device__ __forceinline__ void locate(const PrefixDev& p, const int* pages, int
   *in_page = slot - col * p.a.kv.page;
 }
 
-constexpr int kVPad = 16;  // elements: rows of V in LDS start 32 bytes apart modulo the banks
+// Elements between rows of a wave's own V tile: 4 rows, 64 bytes of each, are
+// read at once and have to lie in different banks of the 64.
+template <int D>
+constexpr int v_pad() {
+  return D == 96 ? 0 : 32;
+}
 
 // One wave's V tile: 32 slots.
 template <int D>
 constexpr int v_tile_elems() {
-  return 32 * (D + kVPad);
+  return 32 * (D + v_pad<D>());
 }
 
 // V^T operand of 16 slots from slot base `kk` and 32 columns from d0.
@@ -196,9 +201,9 @@ template <int D>
 __device__ __forceinline__ s8v read_vt(const short* v, int kk, int d0) {
   const int lane = threadIdx.x & 63;
   const int q = lane & 15;
-  const short* at = v + (kk + 4 * (lane >> 5) + (q >> 2)) * (D + kVPad) + d0 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
+  const short* at = v + (kk + 4 * (lane >> 5) + (q >> 2)) * (D + v_pad<D>()) + d0 + 16 * ((lane >> 4) & 1) + 4 * (q & 3);
   const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
-  const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * (D + kVPad)));
+  const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * (D + v_pad<D>())));
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
@@ -298,7 +303,7 @@ __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages,
 #pragma unroll
     for (int i = 0; i < VL; ++i) {
       const int piece = i * 64 + lane;
-      *reinterpret_cast<s8v*>(v + piece / (D / 8) * (D + kVPad) + 8 * (piece % (D / 8))) = vr[i];
+      *reinterpret_cast<s8v*>(v + piece / (D / 8) * (D + v_pad<D>()) + 8 * (piece % (D / 8))) = vr[i];
     }
     s8v prob[2];
     if (k + 32 > lim_lo) mask_tile(s[0], k, seen);
@@ -317,7 +322,7 @@ __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages,
         if (!__ballot(seen == lim)) continue;
         for (int i = lane; i < 32 * (D / 8); i += 64) {
           const int row = i / (D / 8);
-          if (k + row >= lim) *reinterpret_cast<s8v*>(v + row * (D + kVPad) + 8 * (i % (D / 8))) = s8v{};
+          if (k + row >= lim) *reinterpret_cast<s8v*>(v + row * (D + v_pad<D>()) + 8 * (i % (D / 8))) = s8v{};
         }
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) {
@@ -506,11 +511,14 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
 //
 // LDS. A fetch writes 16 bytes a lane in lane order, so rows lie without
 // padding and the lane picks which 16 bytes of its row it brings: piece c of
-// row r lies at c ^ swizzle(r), chosen so that the 8 rows that a K read and the
-// 4 rows that a transposed V read meet at once lie in different banks.
+// row r lies at c ^ swizzle(r). The 64 banks serve 16 lanes of a 16-byte read
+// at once (lanes 0-3, 12-15 and 20-27, or 4-11, 16-19 and 28-31) and 32 of an
+// 8-byte one; the swizzles give each of them other banks.
 //
 // A wave fetches whole slots' rows, kGroup at a time; with pages of a multiple
-// of kGroup slots the page is the same for the wave and the address scalar.
+// of kGroup slots they lie in one page. Lane g works out where the wave's g-th
+// group of the next step lies, one vector instruction for all of them, and
+// the addresses reach the scalar registers by lane reads.
 constexpr int kTile = 64;
 
 template <int D>
@@ -519,14 +527,13 @@ constexpr int group_slots() {
 }
 template <int D>
 __device__ __forceinline__ int swizzle_k(int r) {
-  return D == 96 ? (r >> 1) & 3 : r & 7;
+  return D == 128 ? r & 15 : D == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
 }
 template <int D>
 __device__ __forceinline__ int swizzle_v(int r) {
-  return D == 96 ? r & 2 : 2 * (r & 3);
+  return D == 128 ? 4 * (r & 3) : D == 64 ? 2 * (r & 2) : 0;
 }
 
-typedef __attribute__((address_space(4))) const int const_int;
 typedef __attribute__((address_space(3))) short lds_short;
 
 // 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
@@ -540,44 +547,55 @@ __device__ __forceinline__ void fetch16(const void* base, uint32_t off, uint32_t
 }
 __device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// A wave's fetches of 32 slots ("half" a tile): kH groups of kGroup slots.
 template <int D, int NW>
 struct Fetch {
   static constexpr int kGroup = group_slots<D>();
-  static constexpr int kN = kTile / (NW * kGroup);  // groups of a wave in a tile
+  static constexpr int kH = 32 / (NW * kGroup);
+  static_assert(kH >= 1 && NW * kGroup % 16 == 0, "every group of a wave swizzles alike");
   uint32_t koff, voff;  // the lane's byte offset in a group's rows
   bool on;              // the lane has a piece
   int wave;
+  int page, in_page;    // of group g of the two halves behind `to`, in lane g < 2 kH
+  const char *kp, *vp;  // first rows of the groups of the last two located halves, in lane g
 
   __device__ __forceinline__ void init(const PrefixDev& p) {
     const int lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane / (D / 8), c = lane % (D / 8);
-    const int row = wave * kGroup + r;  // NW * kGroup is a multiple of 8: every group of the wave swizzles alike
+    const int row = wave * kGroup + r;
     on = r < kGroup;
     koff = 2 * (uint32_t)(r * p.a.kv.kss + 8 * (c ^ swizzle_k<D>(row)));
     voff = 2 * (uint32_t)(r * p.a.kv.vss + 8 * (c ^ swizzle_v<D>(row)));
   }
-  // First slot of group i of the tile at slot0; a group past the end repeats the last one.
-  __device__ __forceinline__ int slot(int slot0, int k1, int i) const {
-    return min(slot0 + (i * NW + wave) * kGroup, (k1 - 1) / kGroup * kGroup);
+  // Starts looking up the pages of the halves from slot0 and slot0 + 32. A
+  // group past the end repeats the last one.
+  __device__ __forceinline__ void look(const PrefixDev& p, const int* table, int slot0, int k1) {
+    const int g = min(threadIdx.x & 63, 2 * kH - 1);
+    const int at = slot0 + (g / kH) * 32 + (g % kH * NW + wave) * kGroup;
+    const int slot = min(at, (k1 - 1) / kGroup * kGroup);
+    const int col = div_by(p.a.kv.by_page, slot);
+    page = table[col];
+    in_page = slot - col * p.a.kv.page;
   }
-  __device__ __forceinline__ void pages(const PrefixDev& p, const const_int* table, int slot0, int k1,
-                                        int (&pg)[kN]) const {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) pg[i] = table[div_by(p.a.kv.by_page, slot(slot0, k1, i))];
-  }
-  __device__ __forceinline__ void tile(const PrefixDev& p, const char* base, long long ps, long long ss, uint32_t off,
-                                       int slot0, int k1, const int (&pg)[kN], uint32_t at) const {
+  // Takes the looked up pages into kp and vp.
+  __device__ __forceinline__ void locate(const PrefixDev& p, int h) {
     const KvView& kv = p.a.kv;
+    if ((unsigned)page >= (unsigned)kv.pages) {
+      flag(p, kKvBadPage);
+      page = 0;
+    }
+    kp = kv.k + 2 * (page * kv.kps + in_page * kv.kss + h * kv.khs);
+    vp = kv.v + 2 * (page * kv.vps + in_page * kv.vss + h * kv.vhs);
+  }
+  // Fetches half `half` of those located, `at` being its place in LDS.
+  __device__ __forceinline__ void half_tile(const char* rows, uint32_t off, int half, uint32_t at) const {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const int s = slot(slot0, k1, i);
-      int page = pg[i];
-      if (page < 0 || page >= kv.pages) {
-        flag(p, kKvBadPage);
-        page = 0;
-      }
-      const char* from = base + 2 * (page * ps + (s - div_by(kv.by_page, s) * kv.page) * ss);
+    for (int i = 0; i < kH; ++i) {
+      const uint64_t a = (uint64_t)(uintptr_t)rows;
+      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)a, half * kH + i);
+      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(a >> 32), half * kH + i);
+      const void* from = (const void*)(uintptr_t)((uint64_t)hi << 32 | lo);
       if (on) fetch16(from, off, at + (i * NW + wave) * kGroup * 2 * D);
     }
   }
@@ -627,12 +645,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   // blocks are dealt to the 8 XCDs in turn: neighbours in the work's order,
   // which read the same part of the prefix, go to one XCD and its L2
   if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
-  const const_int* table = (const_int*)(uintptr_t)x.pages;
-  const KvView& kv = p.a.kv;
   const int k1 = x.k1;
   Rows it = x.it;
-  const char* kbase = kv.k + 2 * it.h * kv.khs;
-  const char* vbase = kv.v + 2 * it.h * kv.vhs;
   it.r0 += 32 * wave;
   const bool live = it.r0 < it.rows;  // waves without rows only fetch
   Wave<DT, D> w;
@@ -641,21 +655,24 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
     F f;
     f.init(p);
     const uint32_t lds = (uint32_t)(uintptr_t)(lds_short*)smem;
-    // K tiles at 0 and 1, V tiles at 2 and 3
-    auto at = [&](int i) { return lds + 2 * kRows * i; };
-    int pg[F::kN], pn[F::kN];  // pages of a tile of V and of K
-    f.pages(p, table, x.k0, k1, pg);
-    f.pages(p, table, x.k0 + 32, k1, pn);
-    f.tile(p, kbase, kv.kps, kv.kss, f.koff, x.k0, k1, pg, at(1));
-    f.tile(p, vbase, kv.vps, kv.vss, f.voff, x.k0, k1, pg, at(2));
-    f.tile(p, kbase, kv.kps, kv.kss, f.koff, x.k0 + 32, k1, pn, at(0));
-    f.pages(p, table, x.k0 + kTile, k1, pg);
-    f.pages(p, table, x.k0 + kTile + 32, k1, pn);
+    // 32 slots' places: K 0 to 3 (two tiles), V 4 to 7
+    auto at = [&](int i) { return lds + kRows * i; };
+    f.look(p, x.pages, x.k0, k1);
+    f.locate(p, it.h);
+    f.half_tile(f.kp, f.koff, 0, at(2));
+    f.half_tile(f.vp, f.voff, 0, at(4));
+    f.half_tile(f.kp, f.koff, 1, at(0));
+    f.half_tile(f.vp, f.voff, 1, at(5));
+    f.look(p, x.pages, x.k0 + 32, k1);
+    f.locate(p, it.h);
+    f.half_tile(f.kp, f.koff, 1, at(1));
+    const char* vlast = f.vp;  // its second half is the next one of V
+    f.look(p, x.pages, x.k0 + 96, k1);
     wait_fetch();
     __syncthreads();
     f16v s[1], t[1];
     if (live) {
-      scores<DT, D>(w, smem + kRows, s);
+      scores<DT, D>(w, smem + kRows, s);  // its place becomes the second K tile's
       if (x.k0 + 32 > k1) mask_tile(s[0], x.k0, k1);
     }
     __syncthreads();
@@ -664,10 +681,13 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
       const short* ks = smem + b * kRows;
       short* vs = smem + (2 + b) * kRows;
       if (k + kTile < k1) {
-        f.tile(p, kbase, kv.kps, kv.kss, f.koff, k + kTile + 32, k1, pn, at(1 - b));
-        f.tile(p, vbase, kv.vps, kv.vss, f.voff, k + kTile, k1, pg, at(3 - b));
-        f.pages(p, table, k + 2 * kTile, k1, pg);
-        f.pages(p, table, k + 2 * kTile + 32, k1, pn);
+        f.locate(p, it.h);  // slots k + 96 .. k + 159
+        f.half_tile(f.kp, f.koff, 0, at(2 - 2 * b));
+        f.half_tile(f.kp, f.koff, 1, at(3 - 2 * b));
+        f.half_tile(vlast, f.voff, 1, at(6 - 2 * b));
+        f.half_tile(f.vp, f.voff, 0, at(7 - 2 * b));
+        vlast = f.vp;
+        f.look(p, x.pages, k + 160, k1);
       } else if (k + kTile > k1) {
         // values behind the end are cleared: a probability of zero must not meet an infinity
         for (int i = threadIdx.x; i < (k + kTile - k1) * (D / 8); i += NW * 64)
