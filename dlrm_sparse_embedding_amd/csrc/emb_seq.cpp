@@ -121,9 +121,10 @@ PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, long lon
   const long long pcap = groups > 0 ? (long long)pwidth * kv.page : 0;
   const long long ocap = (long long)width * kv.page;
   if (pcap > 0) {
-    // Rows of one group and cache head, on average; the wide tiles fetch 4 or 8
-    // slots of a page at a time, with 32-bit offsets among them.
-    p.wide = tokens * m > 64ll * groups && kv.page % 8 == 0 && std::max(kv.kss, kv.vss) < (1ll << 27);
+    // Rows of one group and cache head, on average. The wide tiles fetch 4 or 8
+    // slots of a page at a time, with 32-bit offsets (in 16 bytes) inside a page.
+    const long long slots = std::max(kv.kss, kv.vss), step = std::max(kv.kps, kv.vps);
+    p.wide = tokens * m > 64ll * groups && kv.page % 8 == 0 && slots * kv.page < (1ll << 31) && step < (1ll << 35);
     const int rows = p.wide ? 128 : 32;
     const long long tiles = std::max<long long>(groups, (tokens * m + rows - 1) / rows);
     const long long want = (512 + tiles * kv.heads - 1) / (tiles * kv.heads);

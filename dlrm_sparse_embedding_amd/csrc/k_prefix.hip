@@ -516,9 +516,8 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
 // 8-byte one; the swizzles give each of them other banks.
 //
 // A wave fetches whole slots' rows, kGroup at a time; with pages of a multiple
-// of kGroup slots they lie in one page. Lane g works out where the wave's g-th
-// group of the next step lies, one vector instruction for all of them, and
-// the addresses reach the scalar registers by lane reads.
+// of kGroup slots they lie in one page. Lane g looks up the page of the wave's
+// g-th group of the next step; the addresses are scalar arithmetic.
 constexpr int kTile = 64;
 
 template <int D>
@@ -556,8 +555,7 @@ struct Fetch {
   uint32_t koff, voff;  // the lane's byte offset in a group's rows
   bool on;              // the lane has a piece
   int wave;
-  int page, in_page;    // of group g of the two halves behind `to`, in lane g < 2 kH
-  const char *kp, *vp;  // first rows of the groups of the last two located halves, in lane g
+  int page, in_page;    // of group g of the last two halves looked up, in lane g < 2 kH
 
   __device__ __forceinline__ void init(const PrefixDev& p) {
     const int lane = threadIdx.x & 63;
@@ -578,24 +576,21 @@ struct Fetch {
     page = table[col];
     in_page = slot - col * p.a.kv.page;
   }
-  // Takes the looked up pages into kp and vp.
-  __device__ __forceinline__ void locate(const PrefixDev& p, int h) {
-    const KvView& kv = p.a.kv;
-    if ((unsigned)page >= (unsigned)kv.pages) {
+  __device__ __forceinline__ void check(const PrefixDev& p) {
+    if ((unsigned)page >= (unsigned)p.a.kv.pages) {
       flag(p, kKvBadPage);
       page = 0;
     }
-    kp = kv.k + 2 * (page * kv.kps + in_page * kv.kss + h * kv.khs);
-    vp = kv.v + 2 * (page * kv.vps + in_page * kv.vss + h * kv.vhs);
   }
-  // Fetches half `half` of those located, `at` being its place in LDS.
-  __device__ __forceinline__ void half_tile(const char* rows, uint32_t off, int half, uint32_t at) const {
+  // Fetches half `half` of those looked up, `at` being its place in LDS. ps and
+  // ss are the strides of a page and a slot in 16 bytes.
+  __device__ __forceinline__ void half_tile(const char* base, uint32_t ps, uint32_t ss, uint32_t off, int pages,
+                                            int slots, int half, uint32_t at) const {
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
-      const uint64_t a = (uint64_t)(uintptr_t)rows;
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)a, half * kH + i);
-      const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(a >> 32), half * kH + i);
-      const void* from = (const void*)(uintptr_t)((uint64_t)hi << 32 | lo);
+      const uint32_t pg = __builtin_amdgcn_readlane(pages, half * kH + i);
+      const uint32_t sl = __builtin_amdgcn_readlane(slots, half * kH + i);
+      const char* from = base + (((uint64_t)pg * ps + (uint64_t)(sl * ss)) << 4);
       if (on) fetch16(from, off, at + (i * NW + wave) * kGroup * 2 * D);
     }
   }
@@ -646,7 +641,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   // which read the same part of the prefix, go to one XCD and its L2
   if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
   const int k1 = x.k1;
+  const KvView& kv = p.a.kv;
   Rows it = x.it;
+  const char* kbase = kv.k + 2 * it.h * kv.khs;
+  const char* vbase = kv.v + 2 * it.h * kv.vhs;
   it.r0 += 32 * wave;
   const bool live = it.r0 < it.rows;  // waves without rows only fetch
   Wave<DT, D> w;
@@ -657,16 +655,22 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
     const uint32_t lds = (uint32_t)(uintptr_t)(lds_short*)smem;
     // 32 slots' places: K 0 to 3 (two tiles), V 4 to 7
     auto at = [&](int i) { return lds + kRows * i; };
+    auto fetch_k = [&](int half, int place) {
+      f.half_tile(kbase, kv.kps >> 3, kv.kss >> 3, f.koff, f.page, f.in_page, half, at(place));
+    };
+    auto fetch_v = [&](int page, int in_page, int half, int place) {
+      f.half_tile(vbase, kv.vps >> 3, kv.vss >> 3, f.voff, page, in_page, half, at(place));
+    };
     f.look(p, x.pages, x.k0, k1);
-    f.locate(p, it.h);
-    f.half_tile(f.kp, f.koff, 0, at(2));
-    f.half_tile(f.vp, f.voff, 0, at(4));
-    f.half_tile(f.kp, f.koff, 1, at(0));
-    f.half_tile(f.vp, f.voff, 1, at(5));
+    f.check(p);
+    fetch_k(0, 2);
+    fetch_k(1, 0);
+    fetch_v(f.page, f.in_page, 0, 4);
+    fetch_v(f.page, f.in_page, 1, 5);
     f.look(p, x.pages, x.k0 + 32, k1);
-    f.locate(p, it.h);
-    f.half_tile(f.kp, f.koff, 1, at(1));
-    const char* vlast = f.vp;  // its second half is the next one of V
+    f.check(p);
+    fetch_k(1, 1);
+    int vpage = f.page, vslot = f.in_page;  // the second half of these is the next one of V
     f.look(p, x.pages, x.k0 + 96, k1);
     wait_fetch();
     __syncthreads();
@@ -676,17 +680,18 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
       if (x.k0 + 32 > k1) mask_tile(s[0], x.k0, k1);
     }
     __syncthreads();
-    int b = 0;
-    for (int k = x.k0; k < k1; k += kTile, b ^= 1) {
+    // One step, on the tiles of parity b.
+    auto step = [&](int k, int b) {
       const short* ks = smem + b * kRows;
       short* vs = smem + (2 + b) * kRows;
       if (k + kTile < k1) {
-        f.locate(p, it.h);  // slots k + 96 .. k + 159
-        f.half_tile(f.kp, f.koff, 0, at(2 - 2 * b));
-        f.half_tile(f.kp, f.koff, 1, at(3 - 2 * b));
-        f.half_tile(vlast, f.voff, 1, at(6 - 2 * b));
-        f.half_tile(f.vp, f.voff, 0, at(7 - 2 * b));
-        vlast = f.vp;
+        f.check(p);  // slots k + 96 .. k + 159
+        fetch_k(0, 2 - 2 * b);
+        fetch_k(1, 3 - 2 * b);
+        fetch_v(vpage, vslot, 1, 6 - 2 * b);
+        fetch_v(f.page, f.in_page, 0, 7 - 2 * b);
+        vpage = f.page;
+        vslot = f.in_page;
         f.look(p, x.pages, k + 160, k1);
       } else if (k + kTile > k1) {
         // values behind the end are cleared: a probability of zero must not meet an infinity
@@ -709,6 +714,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
       }
       wait_fetch();
       __syncthreads();
+    };
+    for (int k = x.k0; k < k1; k += 2 * kTile) {
+      step(k, 0);
+      if (k + kTile < k1) step(k + kTile, 1);
     }
   }
   if (live) store_part<DT, D>(p, it, w, part);
