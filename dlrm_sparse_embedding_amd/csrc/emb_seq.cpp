@@ -112,14 +112,23 @@ int norm_rotary_back_blocks(long long tokens, int hq, int hk, int dim) {
 // Parts of the keys. A launch should give every CU several blocks, so few
 // query rows mean many parts; but each part writes and reads back an fp32
 // partial output, so a part is never below 256 slots of a prefix or 128 of an
-// own sequence.
-PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, long long seqs, int groups, int pwidth,
+// own sequence (8 queries over 4096 slots: 512 or 128 slots a part measure the
+// same, over 1000 slots 512 take 20 us for 17).
+//
+// Short own sequences are taken by the blocks of their rows' prefix, spread over
+// its parts: with one part the result is written directly, without partial
+// outputs (24 users' 1200 candidates: 142 -> 128 us). Beyond kOwnInPrefix slots
+// of table width they would hold these blocks up, and get blocks of their own.
+constexpr long long kOwnInPrefix = 256;
+
+PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, int groups, int pwidth,
                        int width) {
   PrefixPlan p{};
   if (tokens == 0) return p;
   const int m = q_heads / kv.heads;
   const long long pcap = groups > 0 ? (long long)pwidth * kv.page : 0;
   const long long ocap = (long long)width * kv.page;
+  const bool with_own = pcap > 0 && ocap <= kOwnInPrefix;
   if (pcap > 0) {
     // Rows of one group and cache head, on average. The wide tiles fetch 4 or 8
     // slots of a page at a time, with 32-bit offsets (in 16 bytes) inside a page.
@@ -128,18 +137,22 @@ PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, long lon
     const int rows = p.wide ? 128 : 32;
     const long long tiles = std::max<long long>(groups, (tokens * m + rows - 1) / rows);
     const long long want = (512 + tiles * kv.heads - 1) / (tiles * kv.heads);
-    p.nps = (int)std::max<long long>(1, std::min<long long>({want, (pcap + 255) / 256, 32}));
+    // an own tile of 32 slots takes a wave about the time of 64 prefix slots
+    const long long own = with_own ? std::max(1, 32 / m) * ((ocap + 31) / 32) * 64 : 0;
+    p.nps = (int)std::max<long long>(1, std::min<long long>({want, (pcap + own + 255) / 256, 32}));
     p.prefix_tiles = groups + tokens * m / rows;
     p.prefix_blocks = p.prefix_tiles * kv.heads * p.nps;
     if (p.wide) p.prefix_blocks = (p.prefix_blocks + 7) / 8 * 8;
   }
-  const long long waves = (tokens * m + 31) / 32 * kv.heads;
-  const long long want = (2048 + waves - 1) / waves;
-  p.nos = (int)std::max<long long>(1, std::min<long long>({want, (ocap + 127) / 128, 32}));
-  p.own_tq = std::max(1, 32 / m);
-  p.own_tiles = seqs + tokens / p.own_tq;
-  p.own_blocks = (p.own_tiles * kv.heads * p.nos + 3) / 4;
-  const size_t rows = (size_t)tokens * q_heads * (p.nps + p.nos);
+  if (!with_own) {
+    p.own_tiles = (tokens * m + 31) / 32;
+    const long long waves = p.own_tiles * kv.heads;
+    const long long want = (2048 + waves - 1) / waves;
+    p.nos = (int)std::max<long long>(1, std::min<long long>({want, (ocap + 127) / 128, 32}));
+    p.own_blocks = (waves * p.nos + 3) / 4;
+  }
+  // the size does not tell whether the prefix blocks take the own slots along
+  const size_t rows = (size_t)tokens * q_heads * (p.nps + std::max(p.nos, 1));
   p.lse_off = (rows * kv.dim * 4 + 255) & ~size_t(255);
   p.bytes = p.lse_off + ((rows * 4 + 255) & ~size_t(255));
   return p;
@@ -413,7 +426,7 @@ static int check_prefix_sizes(const emb_kv* kv, int64_t tokens, int32_t q_heads,
 size_t emb_prefix_attention_workspace_bytes(const emb_kv* kv, int64_t tokens, int32_t q_heads, int32_t groups,
                                             int32_t prefix_width, int32_t table_width) {
   if (check_prefix_sizes(kv, tokens, q_heads, groups, prefix_width, table_width)) return 0;
-  return prefix_plan(kv->v, tokens, q_heads, 0, groups, prefix_width, table_width).bytes;
+  return prefix_plan(kv->v, tokens, q_heads, groups, prefix_width, table_width).bytes;
 }
 
 int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim, const void* q,
@@ -445,8 +458,8 @@ int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim,
     if (!aligned(h->p, 16) || h->ts % 8 != 0 || h->hs % 8 != 0)
       return fail(EMB_E_INVAL, "q and out need 16-byte alignment and strides of multiples of 16 bytes");
   if (!aligned(lse, 4)) return fail(EMB_E_INVAL, "lse is misaligned");
-  const PrefixPlan p = prefix_plan(kv->v, tokens, q_heads, seqs, groups, prefix_width, table_width);
-  if (p.prefix_blocks + p.own_blocks >= (1ll << 24) || p.own_tiles * kv->v.heads * p.nos >= (1ll << 31))
+  const PrefixPlan p = prefix_plan(kv->v, tokens, q_heads, groups, prefix_width, table_width);
+  if (p.prefix_blocks + p.own_blocks >= (1ll << 24) || p.own_tiles * kv->v.heads * std::max(p.nos, 1) >= (1ll << 31))
     return fail(EMB_E_INVAL, "too many sequences or groups for one call");
   if (!ws) return fail(EMB_E_INVAL, "ws is NULL");
   if (!aligned(ws, 16)) return fail(EMB_E_INVAL, "ws is not 16-byte aligned");

@@ -88,7 +88,7 @@ struct PrefixDev {
   FastDiv by_m;
   int nps, nos;
   int prefix_blocks, prefix_tiles;  // tiles: upper bound, blocks = tiles * heads * nps
-  int own_tiles, own_tq;            // tiles of own_tq tokens each: upper bound
+  int own_tiles;                    // tiles of 32 rows
   float* part_o;
   float* part_lse;
 };
@@ -220,14 +220,14 @@ __device__ __forceinline__ float top_of(const f16v (&s)[N]) {
 // Takes N tiles' scores (raw products) into the running maximum. The outputs
 // are rescaled only where a maximum has grown by more than kSlack since the
 // reference was set: any reference gives the same quotient, and the slack
-// keeps the probabilities below 2^15.
-template <int DT, int D, int N>
-__device__ __forceinline__ void refer(const PrefixDev& p, Wave<DT, D>& w, const f16v (&s)[N]) {
-  const float top = both_halves_max(top_of(s)) * p.scale2;
-  if (__ballot(top > w.mx + kSlack)) {
-    const float mx = fmaxf(w.mx, top);
-    const float keep = mx == kNegInf ? 1.f : __builtin_amdgcn_exp2f(w.mx - mx);
-    w.mx = mx;
+// keeps the probabilities below 2^15. Each row goes by its own scores alone.
+template <int DT, int D>
+__device__ __forceinline__ void refer(const PrefixDev& p, Wave<DT, D>& w, float lane_top) {
+  const float top = both_halves_max(lane_top) * p.scale2;
+  const bool up = top > w.mx + kSlack;
+  if (__ballot(up)) {
+    const float keep = up ? __builtin_amdgcn_exp2f(w.mx - top) : 1.f;
+    w.mx = up ? top : w.mx;
     w.sum *= keep;
 #pragma unroll
     for (int d = 0; d < D / 32; ++d)
@@ -269,90 +269,304 @@ __device__ __forceinline__ void mask_tile(f16v& s, int slot0, int seen) {
     if (slot0 + 8 * (i / 4) + h4 + i % 4 >= seen) s[i] = kNegInf;
 }
 
-// One wave over slots k0, k0 + step, .. below k1 in tiles of 32, the keys
-// straight into registers (each is used once) and the values through the
-// wave's own LDS tile. `seen` is the lane's limit, lim_lo and lim_hi the
-// smallest and largest of the wave's; no slot at or beyond lim_hi is read.
-// `token` tells rows of unlike limits apart.
+// The keys of slot lane % 32 of a tile, and the values of the lane's pieces,
+// from (page, slot in it) of the lane's slot.
+template <int D>
+constexpr int kPieces = 32 * D / 8 / 64;  // 16-byte pieces of a V tile for each lane
+
+template <int D>
+__device__ __forceinline__ void load_k(const KvView& kv, int page, int in_page, int h, s8v (&kf)[D / 16]) {
+  const short* kp = reinterpret_cast<const short*>(kv.k) + page * kv.kps + in_page * kv.kss + h * kv.khs;
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+    kf[s] = *reinterpret_cast<const s8v*>(kp + 16 * s + 8 * ((threadIdx.x & 63) >> 5));
+}
+template <int D>
+__device__ __forceinline__ void load_v(const KvView& kv, int page, int in_page, int h, s8v (&vr)[kPieces<D>]) {
+#pragma unroll
+  for (int i = 0; i < kPieces<D>; ++i) {
+    const int piece = i * 64 + (threadIdx.x & 63), row = piece / (D / 8);
+    const int pg = __shfl(page, row, 64), sl = __shfl(in_page, row, 64);
+    vr[i] = *reinterpret_cast<const s8v*>(reinterpret_cast<const short*>(kv.v) + pg * kv.vps + sl * kv.vss +
+                                          h * kv.vhs + 8 * (piece % (D / 8)));
+  }
+}
+// Into the wave's LDS tile; rows outside [lo, hi) as zeros.
+template <int D>
+__device__ __forceinline__ void put_v(short* v, const s8v (&vr)[kPieces<D>], int lo, int hi) {
+#pragma unroll
+  for (int i = 0; i < kPieces<D>; ++i) {
+    const int piece = i * 64 + (threadIdx.x & 63), row = piece / (D / 8);
+    *reinterpret_cast<s8v*>(v + row * (D + v_pad<D>()) + 8 * (piece % (D / 8))) =
+        row >= lo && row < hi ? vr[i] : s8v{};
+  }
+}
+
+// One wave over the prefix slots k0, k0 + step, .. below k1 in tiles of 32, the
+// keys straight into registers (each is used once) and the values through the
+// wave's own LDS tile.
 template <int DT, int D>
 __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages, int h, int k0, int k1, int step,
-                           int seen, int lim_lo, int lim_hi, short* v) {
+                           short* v) {
   const int lane = threadIdx.x & 63;
-  const KvView& kv = p.a.kv;
-  constexpr int VL = 32 * D / 8 / 64;  // 16-byte pieces of a V tile for each lane
-  k1 = min(k1, lim_hi);
+#pragma unroll 1
   for (int k = k0; k < k1; k += step) {
     int page, in_page;
     // slots past the end read the last one again; their scores are masked
-    locate(p, pages, min(k + (lane & 31), lim_hi - 1), &page, &in_page);
-    const short* kp = reinterpret_cast<const short*>(kv.k) + page * kv.kps + in_page * kv.kss + h * kv.khs;
-    s8v kf[D / 16];
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) kf[s] = *reinterpret_cast<const s8v*>(kp + 16 * s + 8 * (lane >> 5));
-    s8v vr[VL];
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int piece = i * 64 + lane, row = piece / (D / 8);
-      const int pg = __shfl(page, row, 64), sl = __shfl(in_page, row, 64);
-      vr[i] = *reinterpret_cast<const s8v*>(reinterpret_cast<const short*>(kv.v) + pg * kv.vps + sl * kv.vss +
-                                            h * kv.vhs + 8 * (piece % (D / 8)));
-    }
+    locate(p, pages, min(k + (lane & 31), k1 - 1), &page, &in_page);
+    s8v kf[D / 16], vr[kPieces<D>];
+    load_k<D>(p.a.kv, page, in_page, h, kf);
+    load_v<D>(p.a.kv, page, in_page, h, vr);
     f16v s[1] = {};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(kf[i], w.q[i], s[0]);
-#pragma unroll
-    for (int i = 0; i < VL; ++i) {
-      const int piece = i * 64 + lane;
-      *reinterpret_cast<s8v*>(v + piece / (D / 8) * (D + v_pad<D>()) + 8 * (piece % (D / 8))) = vr[i];
-    }
+    // values behind the end are cleared: a probability of zero must not meet an infinity
+    put_v<D>(v, vr, 0, k1 - k);
+    __builtin_amdgcn_sched_barrier(0);
     s8v prob[2];
-    if (k + 32 > lim_lo) mask_tile(s[0], k, seen);
-    refer<DT, D, 1>(p, w, s);
+    if (k + 32 > k1) mask_tile(s[0], k, k1);
+    refer<DT, D>(p, w, top_of(s));
     probabilities<DT, D, 1>(p, w, s, prob);
-    if (k + 32 <= lim_lo || lim_lo == lim_hi) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) w.o[d] = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], w.o[d]);
+  }
+}
+
+// ---- own sequences ---------------------------------------------------------
+// The 32 rows of a tile belong to one sequence or to several. Each sequence is
+// taken in tiles of 32 slots by all rows, those of other sequences masked: the
+// matrix units idle less than the memory system needs anyway. The sequences'
+// tiles form one list, so that the next tile's page is looked up while this one
+// is worked on. With several waves to share it, tile t of sequence b goes to
+// wave (b + t) % step: where a sequence is cut does not depend on its
+// neighbours, and neither does a bit of its result.
+
+// Row lane % 32 of the tile.
+struct OwnRow {
+  int b;      // its sequence
+  int seen;   // slots the row sees
+  int first;  // the sequence's first tile of this wave
+  int base;   // tiles of this wave before the sequence's
+  int end;    // behind its tiles for the last row of a sequence, base for its others
+};
+
+// The last i in [lo, hi) with f(i) <= x for each lane, f non-decreasing, f(lo) <= x.
+template <class F>
+__device__ __forceinline__ int lane_find(int lo, int hi, int x, F f) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (f(mid) <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// s0, s1: the sequences among which the tile's rows are.
+__device__ __forceinline__ OwnRow own_row(const PrefixDev& p, const Rows& it, int s0, int s1, int i0, int step) {
+  const int lane = threadIdx.x & 63;
+  const int row = it.r0 + (lane & 31);
+  const int tok = it.t0 + div_by(p.by_m, min(row, it.rows - 1));
+  OwnRow r;
+  int first = tok, n = 1;
+  r.b = tok;
+  if (p.a.offsets) {
+    const int tok0 = __builtin_amdgcn_readlane(tok, 0), tok1 = __builtin_amdgcn_readlane(tok, 31);
+    // 64 sequences' first tokens in the lanes, from the tile's first one
+    int b0 = s0;
+    if (s1 - s0 >= 64) b0 += wave_find(s1 - s0, tok0, [&](int i) { return first_token(p, s0 + i); });
+    const int off = first_token(p, min(b0 + lane, p.a.seqs));
+    if (b0 + 63 >= s1 || __builtin_amdgcn_readlane(off, 63) > tok1) {
+      int at = 0;
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) {
+        const int x = __shfl(off, at + d, 64);
+        if (at + d < 64 && b0 + at + d < s1 && x <= tok) at += d;
+      }
+      r.b = b0 + at;
+      first = __shfl(off, at, 64);
+      n = __shfl(off, min(at + 1, 63), 64) - first;
+    } else {  // many empty sequences among them
+      r.b = lane_find(b0, s1, tok, [&](int i) { return first_token(p, i); });
+      first = first_token(p, r.b);
+      n = first_token(p, min(r.b + 1, p.a.seqs)) - first;
+    }
+    r.b = min(r.b, p.a.seqs - 1);
+  }
+  int len = p.a.lens[r.b];
+  const long long cap = (long long)p.a.width * p.a.kv.page;
+  if (len < 0 || len > cap) {
+    if (row < it.rows) flag(p, kKvBadPage);
+    len = len < 0 ? 0 : (int)cap;
+  }
+  const bool in = row < it.rows && tok >= first && tok < first + n;
+  r.seen = in ? max(len - n + tok - first + 1, 0) : 0;
+  r.first = i0 - (r.b - s0) % step;
+  if (r.first < 0) r.first += step;
+  // the last row of a sequence, which sees the most, carries its tiles; running sums over the rows
+  const int next = __shfl_down(r.b, 1, 64);
+  const bool last = (lane & 31) == 31 || next != r.b || row + 1 >= it.rows;
+  const int tiles = (r.seen + 31) / 32;
+  const int own = last && tiles > r.first ? (tiles - r.first + step - 1) / step : 0;
+  r.end = own;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up(r.end, d, 32);
+    if ((lane & 31) >= d) r.end += x;
+  }
+  r.base = r.end - own;
+  return r;
+}
+
+// Whether any of a lane's values is an infinity or NaN.
+template <int DT, int N>
+__device__ __forceinline__ bool any_special(const s8v (&x)[N]) {
+  typedef unsigned short us8 __attribute__((ext_vector_type(8)));
+  us8 top = __builtin_bit_cast(us8, x[0]) & (unsigned short)0x7fff;
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(us8, x[i]) & (unsigned short)0x7fff);
+  bool some = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) some |= top[i] >= (DT == EMB_BF16 ? 0x7f80 : 0x7c00);
+  return some;
+}
+
+// Tile i of the wave's list.
+struct OwnTile {
+  int b, slot0, lim;  // uniform: the sequence, the first slot, the rows' largest limit
+  int page, in_page;  // of slot lane % 32; slots from lim on repeat the last one below
+};
+__device__ __forceinline__ int own_total(const OwnRow& r) { return __builtin_amdgcn_readlane(r.end, 31); }
+// All but the page; its column of the sequence's page table row.
+__device__ __forceinline__ int own_place(const PrefixDev& p, const OwnRow& r, int i, int step, OwnTile* t) {
+  const int at = __ffsll((unsigned long long)(uint32_t)__ballot(r.end > i)) - 1;
+  t->b = __builtin_amdgcn_readlane(r.b, at);
+  t->slot0 = 32 * (__builtin_amdgcn_readlane(r.first, at) + (i - __builtin_amdgcn_readlane(r.base, at)) * step);
+  t->lim = __builtin_amdgcn_readlane(r.seen, at);
+  const int slot = min(t->slot0 + (int)(threadIdx.x & 31), t->lim - 1);
+  const int col = div_by(p.a.kv.by_page, slot);
+  t->in_page = slot - col * p.a.kv.page;
+  return col;
+}
+__device__ __forceinline__ OwnTile own_look(const PrefixDev& p, const OwnRow& r, int i, int step) {
+  OwnTile t;
+  const int col = own_place(p, r, i, step, &t);
+  t.page = (p.a.table + (long long)t.b * p.a.width)[col];
+  return t;
+}
+
+// The wave's tiles into w, the first one given. A zero probability must not meet
+// an infinity or NaN that its row does not see (0 * infinity), so tiles with such
+// values are left out (the return value tells) and taken by a second call with
+// WINDOWS: one product for each limit among the sequence's rows with the values
+// beyond it cleared, of which each row keeps its own.
+template <int DT, int D, bool WINDOWS>
+__device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, const OwnRow& r, OwnTile next, int h,
+                                          int step, short* v) {
+  const KvView& kv = p.a.kv;
+  const int total = own_total(r);
+  bool left = false;
+#pragma unroll 1
+  for (int i = 0; i < total; ++i) {
+    OwnTile t = next;
+    if ((unsigned)t.page >= (unsigned)kv.pages) {
+      flag(p, kKvBadPage);
+      t.page = 0;
+    }
+    s8v kf[D / 16], vr[kPieces<D>];
+    load_k<D>(kv, t.page, t.in_page, h, kf);
+    load_v<D>(kv, t.page, t.in_page, h, vr);
+    if (i + 1 < total) next = own_look(p, r, i + 1, step);
+    const bool special = __ballot(any_special<DT>(vr));
+    if (special != WINDOWS) {
+      left = true;
+      continue;
+    }
+    f16v s[1] = {};
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) s[0] = mfma<DT>(kf[c], w.q[c], s[0]);
+    const bool mine = r.b == t.b;
+    mask_tile(s[0], t.slot0, mine ? r.seen : 0);
+    if (!WINDOWS) put_v<D>(v, vr, 0, 32);
+    s8v prob[2];
+    refer<DT, D>(p, w, top_of(s));
+    probabilities<DT, D, 1>(p, w, s, prob);
+    if (!WINDOWS) {
 #pragma unroll
       for (int d = 0; d < D / 32; ++d)
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) w.o[d] = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], w.o[d]);
-    } else {
-      // Rows of unlike limits in one tile: a zero probability must not meet a
-      // value that its row does not see (0 * infinity). One product for each
-      // limit, the values beyond it cleared, and each row keeps its own.
-      for (int lim = lim_hi; lim >= lim_lo; --lim) {
-        if (!__ballot(seen == lim)) continue;
-        for (int i = lane; i < 32 * (D / 8); i += 64) {
-          const int row = i / (D / 8);
-          if (k + row >= lim) *reinterpret_cast<s8v*>(v + row * (D + v_pad<D>()) + 8 * (i % (D / 8))) = s8v{};
-        }
+      continue;
+    }
+    int done = 0;  // limits up to this one are through
+    for (int a = 0; a < 32; ++a) {
+      const int lim = __builtin_amdgcn_readlane(r.seen, a);
+      if (__builtin_amdgcn_readlane(r.b, a) != t.b || lim <= done) continue;
+      done = lim;
+      put_v<D>(v, vr, 0, lim - t.slot0);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          f16v o = {};
+      for (int d = 0; d < D / 32; ++d) {
+        f16v o = {};
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) o = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], o);
-          if (seen == lim) {
+        for (int kk = 0; kk < 2; ++kk) o = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], o);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w.o[d][i] += o[i];
-          }
-        }
+        for (int c = 0; c < 16; ++c) w.o[d][c] += mine && r.seen == lim ? o[c] : 0.f;
       }
     }
   }
+  return left;
 }
 
-// Stores the wave's rows as partial output `part`.
+// What the wave has to do of the rows' own slots, into w. `page`: of the first
+// tile's slots (own_look's), where there is one.
 template <int DT, int D>
-__device__ __forceinline__ void store_part(const PrefixDev& p, const Rows& it, Wave<DT, D>& w, int part) {
+__device__ __forceinline__ void own_slots(const PrefixDev& p, Wave<DT, D>& w, const OwnRow& r, int page, int h, int step,
+                                          short* v) {
+  if (own_total(r) == 0) return;
+  OwnTile t;
+  own_place(p, r, 0, step, &t);
+  t.page = page;
+  if (own_tiles<DT, D, false>(p, w, r, t, h, step, v)) own_tiles<DT, D, true>(p, w, r, own_look(p, r, 0, step), h, step, v);
+}
+
+// Stores the wave's rows: as partial output `part`, or, where there is only one
+// part, as the call's result.
+template <int DT, int D>
+__device__ __forceinline__ void store_rows(const PrefixDev& p, const Rows& it, Wave<DT, D>& w, int part) {
   const int lane = threadIdx.x & 63;
   const int row = it.r0 + (lane & 31);
   const float total = both_halves_sum(w.sum);
-  if (row >= it.rows) return;
-  const int j = div_by(p.by_m, row);
-  const int head = it.h * p.m + row - j * p.m;
-  const long long at = ((long long)part * p.a.tokens + it.t0 + j) * p.a.q_heads + head;
   const bool some = !(total == 0.f);  // a NaN counts
-  if (lane < 32) p.part_lse[at] = some ? w.mx - kShift + __log2f(total) : kNegInf;
+  const float z = some ? w.mx - kShift + __log2f(total) : kNegInf;
+  const float inv = some ? 1.f / total : 0.f;
+  const int j = div_by(p.by_m, min(row, it.rows - 1));
+  const int head = it.h * p.m + min(row, it.rows - 1) - j * p.m;
+  if (p.nps + p.nos == 1) {
+    const long long at = (long long)(it.t0 + j) * p.a.q_heads + head;
+    if (row < it.rows && lane < 32 && p.a.lse) p.a.lse[at] = some ? z * 0.6931471805599453f : kNegInf;
+    short* dst = reinterpret_cast<short*>(const_cast<void*>(p.a.out.p)) + (long long)(it.t0 + j) * p.a.out.ts +
+                 head * p.a.out.hs + 8 * (lane >> 5);
+    // lanes l and l + 32 hold 4 columns each of every 8; they trade halves so
+    // that one stores columns 16 i .. + 7 and the other the next 8
+    typedef unsigned u2v __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const f16v& o = w.o[d];
+        const u2v lo = __builtin_amdgcn_permlane32_swap(pack2<DT>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                                        pack2<DT>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), false, false);
+        const u2v hi = __builtin_amdgcn_permlane32_swap(pack2<DT>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                                        pack2<DT>(o[8 * i + 6] * inv, o[8 * i + 7] * inv), false, false);
+        if (row < it.rows) *reinterpret_cast<u4*>(dst + 32 * d + 16 * i) = some ? u4{lo.x, hi.x, lo.y, hi.y} : u4{0, 0, 0, 0};
+      }
+    return;
+  }
+  if (row >= it.rows) return;
+  const long long at = ((long long)part * p.a.tokens + it.t0 + j) * p.a.q_heads + head;
+  if (lane < 32) p.part_lse[at] = z;
   if (!some) return;
-  const float inv = 1.f / total;
   float* dst = p.part_o + at * D + 4 * (lane >> 5);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d)
@@ -366,6 +580,7 @@ __device__ __forceinline__ void store_part(const PrefixDev& p, const Rows& it, W
 // part of the prefix. False where there is none.
 struct PrefixItem {
   Rows it;
+  int s0, s1;  // the group's sequences
   const int* pages;
   int k0, k1;
 };
@@ -376,69 +591,73 @@ __device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows
   *part = id % p.nps;
   const int h = id / p.nps;
   if (h >= p.a.kv.heads) return false;  // the grid is a multiple of 8
-  // tile i of the group whose tiles start at g + (its first row) / rows
-  const int g = wave_find(p.a.groups, tile, [&](int i) { return i + group_token(p, i) * p.m / rows; });
-  const int t0 = group_token(p, g), t1 = group_token(p, g + 1);
-  w->it = Rows{t0, (tile - (g + t0 * p.m / rows)) * rows, (t1 - t0) * p.m, h};
-  if (tile == 0 && *part == 0 && h == 0 && threadIdx.x == 0 &&
-      (p.a.group_offsets[0] != 0 || p.a.group_offsets[p.a.groups] != p.a.seqs))
-    flag(p, kKvBadOffsets);
-  if (w->it.r0 < 0 || w->it.r0 >= w->it.rows) return false;  // the bound counts more tiles than there are
-  int len = p.a.prefix_lens[g];
   const long long cap = (long long)p.a.pwidth * p.a.kv.page;
-  if (len < 0 || len > cap) {
-    if (threadIdx.x == 0) flag(p, kKvBadPage);
-    len = len < 0 ? 0 : (int)cap;
+  auto limit = [&](int n, bool report) {
+    if (n >= 0 && n <= cap) return n;
+    if (report) flag(p, kKvBadPage);
+    return n < 0 ? 0 : (int)cap;
+  };
+  int g, t0, t1, len;
+  if (p.a.groups <= 64) {
+    // A group for each lane; tiles in the order of falling prefix lengths, so
+    // that the longest are not the last to start.
+    const int lane = threadIdx.x & 63, i = min(lane, p.a.groups - 1);
+    const int l = limit(p.a.prefix_lens[i], threadIdx.x < 64 && (int)threadIdx.x < p.a.groups);
+    const int c0 = min(max(p.a.group_offsets[i], 0), p.a.seqs), c1 = min(max(p.a.group_offsets[i + 1], 0), p.a.seqs);
+    const int a0 = first_token(p, c0), a1 = first_token(p, c1);
+    const int n = lane < p.a.groups && a1 > a0 ? ((a1 - a0) * p.m + rows - 1) / rows : 0;
+    int at = 0;  // tiles before this group's
+    for (int j = 0; j < p.a.groups; ++j) {
+      const int lj = __builtin_amdgcn_readlane(l, j), nj = __builtin_amdgcn_readlane(n, j);
+      at += lj > l || (lj == l && j < lane) ? nj : 0;
+    }
+    const uint64_t mine = __ballot(tile >= at && tile < at + n);
+    if (!mine) return false;
+    g = __ffsll((unsigned long long)mine) - 1;
+    t0 = __builtin_amdgcn_readlane(a0, g);
+    t1 = __builtin_amdgcn_readlane(a1, g);
+    len = __builtin_amdgcn_readlane(l, g);
+    w->s0 = __builtin_amdgcn_readlane(c0, g);
+    w->s1 = __builtin_amdgcn_readlane(c1, g);
+    w->it = Rows{t0, (tile - __builtin_amdgcn_readlane(at, g)) * rows, (t1 - t0) * p.m, h};
+  } else {
+    // tile i of the group whose tiles start at g + (its first row) / rows: a
+    // bound that counts more tiles than there are
+    g = wave_find(p.a.groups, tile, [&](int i) { return i + group_token(p, i) * p.m / rows; });
+    t0 = group_token(p, g);
+    t1 = group_token(p, g + 1);
+    w->it = Rows{t0, (tile - (g + t0 * p.m / rows)) * rows, (t1 - t0) * p.m, h};
+    if (w->it.r0 < 0 || w->it.r0 >= w->it.rows) return false;
+    len = limit(p.a.prefix_lens[g], threadIdx.x == 0);
+    w->s0 = min(max(p.a.group_offsets[g], 0), p.a.seqs);
+    w->s1 = min(max(p.a.group_offsets[g + 1], 0), p.a.seqs);
   }
-  const int chunk = max(256, ((len + p.nps - 1) / p.nps + 127) & ~127);
+  const int chunk = max(128, ((len + p.nps - 1) / p.nps + 127) & ~127);
   w->k0 = (int)min((long long)*part * chunk, (long long)len);
   w->k1 = min(w->k0 + chunk, len);
   w->pages = p.a.prefix_table + (long long)g * p.a.pwidth;
   return true;
 }
 
-// Own sequences: each wave of block `block` for itself takes a tile of rows, a
-// cache head and a part of the sequence; part fastest, then the tile, then the
-// cache head.
-template <int DT, int D>
-__device__ void own_part(const PrefixDev& p, int block, short* v) {
-  const int lane = threadIdx.x & 63;
+// Own sequences on their own: each wave of block `block` for itself takes a tile
+// of 32 rows, a cache head and a part of the rows' own slots; part fastest,
+// then the tile, then the cache head. False where there is none.
+__device__ __forceinline__ bool own_item(const PrefixDev& p, int block, Rows* it, int* part) {
   int id = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int part = id % p.nos;
+  *part = id % p.nos;
   id /= p.nos;
   const int tile = id % p.own_tiles;
   const int h = id / p.own_tiles;
-  if (h >= p.a.kv.heads) return;
-  const int b = wave_find(p.a.seqs, tile, [&](int i) { return i + first_token(p, i) / p.own_tq; });
-  const int t0 = first_token(p, b), t1 = first_token(p, b + 1);
-  const int j0 = (tile - (b + t0 / p.own_tq)) * p.own_tq;  // first token of the tile, counted from t0
-  if (tile == 0 && part == 0 && h == 0 && lane == 0 && p.a.offsets &&
-      (p.a.offsets[0] != 0 || p.a.offsets[p.a.seqs] != p.a.tokens))
+  *it = Rows{0, tile * 32, p.a.tokens * p.m, h};
+  return h < p.a.kv.heads;
+}
+
+// One thread's look at the offsets' ends.
+__device__ __forceinline__ void check_offsets(const PrefixDev& p) {
+  if (blockIdx.x != 0 || threadIdx.x != 0) return;
+  if (p.a.offsets && (p.a.offsets[0] != 0 || p.a.offsets[p.a.seqs] != p.a.tokens)) flag(p, kKvBadOffsets);
+  if (p.a.groups > 0 && (p.a.group_offsets[0] != 0 || p.a.group_offsets[p.a.groups] != p.a.seqs))
     flag(p, kKvBadOffsets);
-  const int n = t1 - t0;
-  if (j0 < 0 || j0 >= n) return;
-  int len = p.a.lens[b];
-  const long long cap = (long long)p.a.width * p.a.kv.page;
-  if (len < 0 || len > cap) {
-    if (lane == 0) flag(p, kKvBadPage);
-    len = len < 0 ? 0 : (int)cap;
-  }
-  const int j1 = min(j0 + p.own_tq, n);
-  const int lim_lo = max(len - n + j0 + 1, 0), lim_hi = max(len - n + j1, 0);
-  const int chunk = max(128, ((lim_hi + p.nos - 1) / p.nos + 31) & ~31);
-  const int k0 = part * chunk;
-  // more than 32 query heads of one cache head: a token takes several tiles of rows
-  for (int r0 = j0 * p.m; r0 < j1 * p.m; r0 += 32) {
-    const Rows it{t0, r0, j1 * p.m, h};
-    Wave<DT, D> w;
-    load_q<DT, D>(p, it, w);
-    const int j = div_by(p.by_m, min(r0 + (lane & 31), it.rows - 1));
-    const int seen = max(len - n + j + 1, 0);
-    if (k0 < lim_hi)
-      wave_slots<DT, D>(p, w, p.a.table + (long long)b * p.a.width, h, k0, min(k0 + chunk, lim_hi), 32, seen, lim_lo,
-                        lim_hi, v);
-    store_part<DT, D>(p, it, w, p.nps + part);
-  }
 }
 
 // Few rows: a block takes one tile of 32 rows, a cache head and a part of the
@@ -451,13 +670,30 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   short* v = reinterpret_cast<short*>(smem) + wave * v_tile_elems<D>();
   Wave<DT, D> w;
-  if ((int)blockIdx.x < p.prefix_blocks) {
-    PrefixItem x;
-    int part;
+  check_offsets(p);
+  const bool prefix = (int)blockIdx.x < p.prefix_blocks;
+  PrefixItem x;
+  int part;
+  if (prefix) {
     if (!prefix_item(p, blockIdx.x, 32, &x, &part)) return;
-    const Rows it = x.it;
-    load_q<DT, D>(p, it, w);
-    wave_slots<DT, D>(p, w, x.pages, it.h, x.k0 + 32 * wave, x.k1, 128, x.k1, x.k1, x.k1, v);
+  } else {
+    if (!own_item(p, blockIdx.x - p.prefix_blocks, &x.it, &part)) return;
+    x.s0 = 0;
+    x.s1 = p.a.seqs;
+  }
+  const Rows it = x.it;
+  load_q<DT, D>(p, it, w);
+  const bool own = !prefix || p.nos == 0;
+  const int step = prefix ? p.nps * 4 : p.nos;
+  OwnRow r;
+  int page = 0;
+  if (own) {
+    r = own_row(p, it, x.s0, x.s1, prefix ? part * 4 + wave : part, step);
+    if (own_total(r) > 0) page = own_look(p, r, 0, step).page;
+  }
+  if (prefix) wave_slots<DT, D>(p, w, x.pages, it.h, x.k0 + 32 * wave, x.k1, 128, v);
+  if (own) own_slots<DT, D>(p, w, r, page, it.h, step, v);
+  if (prefix) {
     // join: waves 2 and 3 into 0 and 1, then 1 into 0
     float* so = reinterpret_cast<float*>(smem);
     float* sm = so + 2 * 32 * OS;
@@ -493,10 +729,9 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
           }
       }
     }
-    if (wave == 0) store_part<DT, D>(p, it, w, part);
-    return;
+    if (wave > 0) return;
   }
-  own_part<DT, D>(p, blockIdx.x - p.prefix_blocks, v);
+  store_rows<DT, D>(p, it, w, prefix ? part : p.nps + part);
 }
 
 // Many rows: a block takes NW * 32 rows of one cache head and a part of the
@@ -516,8 +751,8 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
 // 8-byte one; the swizzles give each of them other banks.
 //
 // A wave fetches whole slots' rows, kGroup at a time; with pages of a multiple
-// of kGroup slots they lie in one page. Lane g looks up the page of the wave's
-// g-th group of the next step; the addresses are scalar arithmetic.
+// of kGroup slots they lie in one page. The lanes look up the pages of the
+// wave's next 64 groups at once; the addresses are scalar arithmetic.
 constexpr int kTile = 64;
 
 template <int D>
@@ -537,25 +772,37 @@ typedef __attribute__((address_space(3))) short lds_short;
 
 // 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
 // The compiler does not see the transfer: the caller waits (wait_fetch) and
-// passes a barrier before anyone reads.
-__device__ __forceinline__ void fetch16(const void* base, uint32_t off, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
+// passes a barrier before anyone reads. It does not see the instruction's
+// hazards either: a base that a vector instruction wrote would have to be five
+// wait states old, so a scalar one copies it, and that copy is the wait state
+// which m0 needs.
+__device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at) {
+  uint64_t from;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(from)
                : "s"(at), "v"(off), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 __device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// A wave's fetches of 32 slots ("half" a tile): kH groups of kGroup slots.
+// A wave's fetches of 32 slots ("half" a tile): kH groups of kGroup slots. Lane l
+// holds the addresses of group l % kH of half l / kH - 1 of a window of 64 / kH
+// halves.
 template <int D, int NW>
 struct Fetch {
   static constexpr int kGroup = group_slots<D>();
   static constexpr int kH = 32 / (NW * kGroup);
+  static constexpr int kPairs = 32 / kH;  // of halves, in a window
   static_assert(kH >= 1 && NW * kGroup % 16 == 0, "every group of a wave swizzles alike");
+  struct Half {
+    uint64_t k[kH], v[kH];  // uniform: where its groups' rows are
+  };
   uint32_t koff, voff;  // the lane's byte offset in a group's rows
   bool on;              // the lane has a piece
   int wave;
-  int page, in_page;    // of group g of the last two halves looked up, in lane g < 2 kH
+  uint64_t k, v;        // of the window in use
+  int page, in_page;    // of the next one
+  int pair, window;     // the next pair of the window in use; the last window looked up
 
   __device__ __forceinline__ void init(const PrefixDev& p) {
     const int lane = threadIdx.x & 63;
@@ -565,63 +812,115 @@ struct Fetch {
     on = r < kGroup;
     koff = 2 * (uint32_t)(r * p.a.kv.kss + 8 * (c ^ swizzle_k<D>(row)));
     voff = 2 * (uint32_t)(r * p.a.kv.vss + 8 * (c ^ swizzle_v<D>(row)));
+    k = v = 0;
+    page = in_page = pair = window = 0;
   }
-  // Starts looking up the pages of the halves from slot0 and slot0 + 32. A
+  // Starts looking up the pages of window `window` of the slots [k0, k1). A
   // group past the end repeats the last one.
-  __device__ __forceinline__ void look(const PrefixDev& p, const int* table, int slot0, int k1) {
-    const int g = min(threadIdx.x & 63, 2 * kH - 1);
-    const int at = slot0 + (g / kH) * 32 + (g % kH * NW + wave) * kGroup;
-    const int slot = min(at, (k1 - 1) / kGroup * kGroup);
+  __device__ __forceinline__ void look(const PrefixDev& p, const int* table, int k0, int k1) {
+    const int l = threadIdx.x & 63;
+    const long long at = k0 + (2 * kPairs * (long long)window + l / kH - 1) * 32 + (l % kH * NW + wave) * kGroup;
+    const int slot = (int)min(max(at, (long long)k0), (long long)((k1 - 1) / kGroup * kGroup));
     const int col = div_by(p.a.kv.by_page, slot);
     page = table[col];
     in_page = slot - col * p.a.kv.page;
   }
-  __device__ __forceinline__ void check(const PrefixDev& p) {
-    if ((unsigned)page >= (unsigned)p.a.kv.pages) {
+  __device__ __forceinline__ void turn_to_next(const PrefixDev& p, int h) {
+    const KvView& kv = p.a.kv;
+    if ((unsigned)page >= (unsigned)kv.pages) {
       flag(p, kKvBadPage);
       page = 0;
     }
+    k = (uint64_t)(kv.k + 2 * (page * kv.kps + in_page * kv.kss + h * kv.khs));
+    v = (uint64_t)(kv.v + 2 * (page * kv.vps + in_page * kv.vss + h * kv.vhs));
   }
-  // Fetches half `half` of those looked up, `at` being its place in LDS. ps and
-  // ss are the strides of a page and a slot in 16 bytes.
-  __device__ __forceinline__ void half_tile(const char* base, uint32_t ps, uint32_t ss, uint32_t off, int pages,
-                                            int slots, int half, uint32_t at) const {
+  static __device__ __forceinline__ uint64_t lane_of(uint64_t x, int l) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)x, l), hi = __builtin_amdgcn_readlane((int)(x >> 32), l);
+    return (uint64_t)hi << 32 | lo;
+  }
+  // The next two halves.
+  __device__ __forceinline__ void take(const PrefixDev& p, const int* table, int h, int k0, int k1, Half* a, Half* b) {
+    if (pair == kPairs) {
+      pair = 0;
+      turn_to_next(p, h);
+    }
+    if (pair == kPairs / 2) {
+      ++window;
+      look(p, table, k0, k1);
+    }
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
-      const uint32_t pg = __builtin_amdgcn_readlane(pages, half * kH + i);
-      const uint32_t sl = __builtin_amdgcn_readlane(slots, half * kH + i);
-      const char* from = base + (((uint64_t)pg * ps + (uint64_t)(sl * ss)) << 4);
-      if (on) fetch16(from, off, at + (i * NW + wave) * kGroup * 2 * D);
+      a->k[i] = lane_of(k, 2 * pair * kH + i);
+      a->v[i] = lane_of(v, 2 * pair * kH + i);
+      b->k[i] = lane_of(k, (2 * pair + 1) * kH + i);
+      b->v[i] = lane_of(v, (2 * pair + 1) * kH + i);
     }
+    ++pair;
+  }
+  // Fetches a half's rows into LDS at `at`.
+  __device__ __forceinline__ void rows(const uint64_t (&from)[kH], uint32_t off, uint32_t at) const {
+#pragma unroll
+    for (int i = 0; i < kH; ++i)
+      if (on) fetch16(from[i], off, at + (i * NW + wave) * kGroup * 2 * D);
   }
 };
 
-// The scores of 32 slots: K (rows of LDS at k) by the wave's queries.
-template <int DT, int D>
-__device__ __forceinline__ void scores(const Wave<DT, D>& w, const short* k, f16v (&s)[1]) {
+// The wave's operands of 32 slots' keys (rows of LDS at k).
+template <int D>
+__device__ __forceinline__ void read_k(const short* k, s8v (&kf)[D / 16]) {
   const int lane = threadIdx.x & 63, r = lane & 31;
   const int sw = swizzle_k<D>(r) ^ (lane >> 5);
-  s[0] = f16v{};
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i)
-    s[0] = mfma<DT>(*reinterpret_cast<const s8v*>(k + r * D + 8 * ((2 * i) ^ sw)), w.q[i], s[0]);
+  for (int i = 0; i < D / 16; ++i) kf[i] = *reinterpret_cast<const s8v*>(k + r * D + 8 * ((2 * i) ^ sw));
 }
 
-// The outputs' product with V (rows of LDS at v) of 32 slots.
+// The outputs' product with V (rows of LDS at v) of 16 slots.
 template <int DT, int D>
-__device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, const s8v (&prob)[2]) {
+__device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, int kk, const s8v& prob) {
   const int lane = threadIdx.x & 63, q = lane & 15;
   const int r = 4 * (lane >> 5) + (q >> 2);
   const int c = 2 * ((lane >> 4) & 1) + ((q & 3) >> 1), sw = swizzle_v<D>(r);  // the same for r + 8
 #pragma unroll
-  for (int kk = 0; kk < 2; ++kk)
+  for (int d = 0; d < D / 32; ++d) {
+    const short* at = v + (16 * kk + r) * D + 8 * ((4 * d + c) ^ sw) + 4 * (q & 1);
+    const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
+    const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D));
+    w.o[d] = mfma<DT>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), prob, w.o[d]);
+  }
+}
+
+// 32 slots: their scores `s` (maximum `top`) become probabilities and meet V,
+// while the matrix units make the next 32 slots' scores `t` of the keys kf. One
+// stream of instructions in which every product is followed by the vector
+// work of about its own time; left to itself the compiler puts the LDS reads
+// right before their use and waits for each. NEXT: kf then takes the keys at k.
+template <int DT, int D, bool NEXT>
+__device__ __forceinline__ void half_step(const PrefixDev& p, Wave<DT, D>& w, f16v (&s)[1], f16v (&t)[1], float& top,
+                                          s8v (&kf)[D / 16], const short* v, const short* k) {
+  refer<DT, D>(p, w, top);
+  t[0] = f16v{};
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) {
-      const short* at = v + (16 * kk + r) * D + 8 * ((4 * d + c) ^ sw) + 4 * (q & 1);
-      const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
-      const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D));
-      w.o[d] = mfma<DT>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), prob[kk], w.o[d]);
-    }
+  for (int i = 0; i < D / 16; ++i) t[0] = mfma<DT>(kf[i], w.q[i], t[0]);
+  s8v prob[2];
+  probabilities<DT, D, 1>(p, w, s, prob);
+  times_v<DT, D>(w, v, 0, prob[0]);
+  if (NEXT) read_k<D>(k, kf);
+  times_v<DT, D>(w, v, 1, prob[1]);
+  top = top_of(t);
+  constexpr int kMfma = 0x8, kValu = 0x2, kLds = 0x100;
+  __builtin_amdgcn_sched_group_barrier(kLds, D / 16, 0);  // V of slots 0 .. 15
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    if (i >= D / 32) __builtin_amdgcn_sched_group_barrier(kLds, 2, 0);  // and of 16 .. 31
+    __builtin_amdgcn_sched_group_barrier(kValu, 640 / D, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+    if (NEXT && i < D / 32) __builtin_amdgcn_sched_group_barrier(kLds, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(kValu, 6, 0);
+  }
 }
 
 template <int DT, int D, int NW>
@@ -630,54 +929,73 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   constexpr int kRows = kTile * D;  // elements of a tile
   constexpr int kWide = 4 * kRows, kOwn = NW * v_tile_elems<D>();
   __shared__ __attribute__((aligned(1024))) short smem[kWide > kOwn ? kWide : kOwn];
+  __shared__ OwnRow s_own[NW][32];
+  __shared__ int s_page[NW][32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if ((int)blockIdx.x >= p.prefix_blocks) {
-    own_part<DT, D>(p, blockIdx.x - p.prefix_blocks, smem + wave * v_tile_elems<D>());
-    return;
-  }
+  check_offsets(p);
+  const bool prefix = (int)blockIdx.x < p.prefix_blocks;
   PrefixItem x;
   int part;
-  // blocks are dealt to the 8 XCDs in turn: neighbours in the work's order,
-  // which read the same part of the prefix, go to one XCD and its L2
-  if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
+  if (prefix) {
+    // blocks are dealt to the 8 XCDs in turn: neighbours in the work's order,
+    // which read the same part of the prefix, go to one XCD and its L2
+    if (!prefix_item(p, xcd_remap(blockIdx.x, p.prefix_blocks), NW * 32, &x, &part)) return;
+  } else {
+    if (!own_item(p, blockIdx.x - p.prefix_blocks, &x.it, &part)) return;
+    x.s0 = 0;
+    x.s1 = p.a.seqs;
+    x.k0 = x.k1 = 0;
+  }
   const int k1 = x.k1;
   const KvView& kv = p.a.kv;
   Rows it = x.it;
-  const char* kbase = kv.k + 2 * it.h * kv.khs;
-  const char* vbase = kv.v + 2 * it.h * kv.vhs;
-  it.r0 += 32 * wave;
+  it.h = __builtin_amdgcn_readfirstlane(it.h);
+  if (prefix) it.r0 += 32 * wave;
   const bool live = it.r0 < it.rows;  // waves without rows only fetch
   Wave<DT, D> w;
   load_q<DT, D>(p, it, w);
-  if (x.k0 < k1) {
-    F f;
-    f.init(p);
-    const uint32_t lds = (uint32_t)(uintptr_t)(lds_short*)smem;
-    // 32 slots' places: K 0 to 3 (two tiles), V 4 to 7
-    auto at = [&](int i) { return lds + kRows * i; };
-    auto fetch_k = [&](int half, int place) {
-      f.half_tile(kbase, kv.kps >> 3, kv.kss >> 3, f.koff, f.page, f.in_page, half, at(place));
-    };
-    auto fetch_v = [&](int page, int in_page, int half, int place) {
-      f.half_tile(vbase, kv.vps >> 3, kv.vss >> 3, f.voff, page, in_page, half, at(place));
-    };
+  const bool some = x.k0 < k1, own = live && (!prefix || p.nos == 0);
+  const int own_step = prefix ? p.nps : p.nos;
+  F f;
+  f.init(p);
+  typename F::Half ha{}, hb{};
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_short*)smem;
+  // 32 slots' places: K 0 to 3 (two tiles), V 4 to 7
+  auto fetch_k = [&](const typename F::Half& h, int place) { f.rows(h.k, f.koff, lds + kRows * place); };
+  auto fetch_v = [&](const typename F::Half& h, int place) { f.rows(h.v, f.voff, lds + kRows * place); };
+  if (some) {
     f.look(p, x.pages, x.k0, k1);
-    f.check(p);
-    fetch_k(0, 2);
-    fetch_k(1, 0);
-    fetch_v(f.page, f.in_page, 0, 4);
-    fetch_v(f.page, f.in_page, 1, 5);
-    f.look(p, x.pages, x.k0 + 32, k1);
-    f.check(p);
-    fetch_k(1, 1);
-    int vpage = f.page, vslot = f.in_page;  // the second half of these is the next one of V
-    f.look(p, x.pages, x.k0 + 96, k1);
+    f.turn_to_next(p, it.h);
+    f.take(p, x.pages, it.h, x.k0, k1, &ha, &hb);
+    fetch_k(hb, 2);
+    fetch_v(hb, 4);
+    f.take(p, x.pages, it.h, x.k0, k1, &ha, &hb);
+    fetch_k(ha, 0);
+    fetch_v(ha, 5);
+    fetch_k(hb, 1);
+  }
+  // What the own slots need is looked up while the first tiles are on their way.
+  if (own) {
+    const OwnRow r = own_row(p, it, x.s0, x.s1, part, own_step);
+    const int page = own_total(r) > 0 ? own_look(p, r, 0, own_step).page : 0;
+    if ((threadIdx.x & 63) < 32) {
+      s_own[wave][threadIdx.x & 31] = r;
+      s_page[wave][threadIdx.x & 31] = page;
+    }
+  }
+  if (some) {
     wait_fetch();
     __syncthreads();
     f16v s[1], t[1];
+    s8v kf[D / 16];
+    float top = 0.f;
     if (live) {
-      scores<DT, D>(w, smem + kRows, s);  // its place becomes the second K tile's
+      read_k<D>(smem + kRows, kf);  // its place becomes the second K tile's
+      s[0] = f16v{};
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(kf[i], w.q[i], s[0]);
       if (x.k0 + 32 > k1) mask_tile(s[0], x.k0, k1);
+      top = top_of(s);
     }
     __syncthreads();
     // One step, on the tiles of parity b.
@@ -685,14 +1003,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
       const short* ks = smem + b * kRows;
       short* vs = smem + (2 + b) * kRows;
       if (k + kTile < k1) {
-        f.check(p);  // slots k + 96 .. k + 159
-        fetch_k(0, 2 - 2 * b);
-        fetch_k(1, 3 - 2 * b);
-        fetch_v(vpage, vslot, 1, 6 - 2 * b);
-        fetch_v(f.page, f.in_page, 0, 7 - 2 * b);
-        vpage = f.page;
-        vslot = f.in_page;
-        f.look(p, x.pages, k + 160, k1);
+        fetch_v(hb, 6 - 2 * b);  // slots k + 64 ..
+        f.take(p, x.pages, it.h, x.k0, k1, &ha, &hb);
+        fetch_k(ha, 2 - 2 * b);  // slots k + 96 ..
+        fetch_v(ha, 7 - 2 * b);
+        fetch_k(hb, 3 - 2 * b);
       } else if (k + kTile > k1) {
         // values behind the end are cleared: a probability of zero must not meet an infinity
         for (int i = threadIdx.x; i < (k + kTile - k1) * (D / 8); i += NW * 64)
@@ -700,17 +1015,17 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
         __syncthreads();
       }
       if (live) {
-        s8v prob[2];
-        refer<DT, D, 1>(p, w, s);
-        scores<DT, D>(w, ks, t);
-        probabilities<DT, D, 1>(p, w, s, prob);
-        times_v<DT, D>(w, vs, prob);
-        if (k + 64 > k1) mask_tile(t[0], k + 32, k1);
-        refer<DT, D, 1>(p, w, t);
-        scores<DT, D>(w, ks + 32 * D, s);
-        probabilities<DT, D, 1>(p, w, t, prob);
-        times_v<DT, D>(w, vs + 32 * D, prob);
-        if (k + 96 > k1) mask_tile(s[0], k + 64, k1);
+        read_k<D>(ks, kf);
+        half_step<DT, D, true>(p, w, s, t, top, kf, vs, ks + 32 * D);
+        if (k + 64 > k1) {
+          mask_tile(t[0], k + 32, k1);
+          top = top_of(t);
+        }
+        half_step<DT, D, false>(p, w, t, s, top, kf, vs + 32 * D, nullptr);
+        if (k + 96 > k1) {
+          mask_tile(s[0], k + 64, k1);
+          top = top_of(s);
+        }
       }
       wait_fetch();
       __syncthreads();
@@ -720,7 +1035,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
       if (k + kTile < k1) step(k + kTile, 1);
     }
   }
-  if (live) store_part<DT, D>(p, it, w, part);
+  if (!live) return;
+  if (own)
+    own_slots<DT, D>(p, w, s_own[wave][threadIdx.x & 31], s_page[wave][threadIdx.x & 31], it.h, own_step,
+                     smem + wave * v_tile_elems<D>());
+  store_rows<DT, D>(p, it, w, prefix ? part : p.nps + part);
 }
 
 // Joins the parts of each (token, query head): 32 lanes, 4 columns each.
@@ -742,10 +1061,17 @@ __global__ __launch_bounds__(256) void k_join(PrefixDev p) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) total += __shfl_xor(total, d, 32);
     f4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int i = 0; i < parts; ++i) {
-      const float wgt = i < 32 ? __shfl(z0, i, 32) : __shfl(z1, i - 32, 32);
-      if (wgt == 0.f) continue;  // an empty part holds nothing, not zeros
-      if (l < D / 4) acc += *reinterpret_cast<const f4*>(p.part_o + (i * rows + row) * D + 4 * l) * wgt;
+    // eight parts' loads at once; an empty part holds nothing, not zeros
+    for (int i = 0; i < parts; i += 8) {
+      f4 x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = *reinterpret_cast<const f4*>(p.part_o + (min(i + k, parts - 1) * rows + row) * D + 4 * min(l, D / 4 - 1));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float wgt = i < 32 ? __shfl(z0, i + k, 32) : __shfl(z1, i + k - 32, 32);
+        if (i + k < parts && wgt != 0.f) acc += x[k] * wgt;
+      }
     }
     const bool some = !(total == 0.f);
     const float inv = some ? 1.f / total : 0.f;
@@ -767,6 +1093,7 @@ hipError_t launch(const PrefixDev& p, int blocks, bool wide, hipStream_t st) {
   if (wide) k_attend_wide<DT, D, 4><<<blocks, 256, 0, st>>>(p);
   else k_attend<DT, D><<<blocks, 256, 0, st>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
+  if (p.nps + p.nos == 1) return hipSuccess;
   const long long rows = (long long)p.a.tokens * p.a.q_heads;
   k_join<DT, D><<<(unsigned)std::min<long long>((rows + 7) / 8, 1 << 20), 256, 0, st>>>(p);
   return hipGetLastError();
@@ -787,7 +1114,6 @@ hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& plan, 
   p.nos = plan.nos;
   p.prefix_tiles = (int)plan.prefix_tiles;
   p.prefix_blocks = (int)plan.prefix_blocks;
-  p.own_tq = plan.own_tq;
   p.own_tiles = (int)plan.own_tiles;
   p.part_o = reinterpret_cast<float*>(ws + plan.o_off);
   p.part_lse = reinterpret_cast<float*>(ws + plan.lse_off);

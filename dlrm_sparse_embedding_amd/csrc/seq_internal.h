@@ -125,14 +125,12 @@ struct PrefixArgs {
 struct PrefixPlan {
   int nps, nos;
   bool wide;   // prefix tiles of 128 rows that share their keys in LDS, else 32
-  int own_tq;  // query tokens of an own tile
   long long prefix_tiles, prefix_blocks, own_tiles, own_blocks;
   size_t o_off;     // partial outputs fp32 [nps + nos][tokens][q_heads][dim]
   size_t lse_off;   // fp32 [nps + nos][tokens][q_heads]
   size_t bytes;
 };
-// seqs only sets the grid, not the workspace.
-PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, long long seqs, int groups, int pwidth,
+PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, int groups, int pwidth,
                        int width);
 hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& p, char* ws, hipStream_t st);
 
