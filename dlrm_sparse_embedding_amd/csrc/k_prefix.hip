@@ -190,12 +190,6 @@ constexpr int v_pad() {
   return D == 96 ? 0 : 32;
 }
 
-// One wave's V tile: 32 slots.
-template <int D>
-constexpr int v_tile_elems() {
-  return 32 * (D + v_pad<D>());
-}
-
 // V^T operand of 16 slots from slot base `kk` and 32 columns from d0.
 template <int D>
 __device__ __forceinline__ s8v read_vt(const short* v, int kk, int d0) {
@@ -334,6 +328,61 @@ __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages,
   }
 }
 
+// ---- values in LDS as fetches leave them: 16-byte piece c of row r at c ^ swizzle(r)
+
+template <int D>
+__device__ __forceinline__ int swizzle_k(int r) {
+  return D == 128 ? r & 15 : D == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
+}
+template <int D>
+__device__ __forceinline__ int swizzle_v(int r) {
+  return D == 128 ? 4 * (r & 3) : D == 64 ? 2 * (r & 2) : 0;
+}
+
+typedef __attribute__((address_space(3))) short lds_short;
+
+// 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
+// The compiler does not see the transfer: the caller waits (wait_fetch) and
+// passes a barrier before anyone reads. It does not see the instruction's
+// hazards either: a base that a vector instruction wrote would have to be five
+// wait states old, so a scalar one copies it, and that copy is the wait state
+// which m0 needs.
+__device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at) {
+  uint64_t from;
+  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+               : "=&s"(from)
+               : "s"(at), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// The same with an address for each lane.
+__device__ __forceinline__ void fetch16(uint64_t from, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(at), "v"(from)
+               : "memory", "m0");
+}
+
+// V^T operand of 16 slots from slot 16 kk and 32 columns from 32 d (rows of LDS at v).
+template <int D>
+__device__ __forceinline__ s8v operand_v(const short* v, int kk, int d) {
+  const int lane = threadIdx.x & 63, q = lane & 15;
+  const int r = 4 * (lane >> 5) + (q >> 2);
+  const int c = 2 * ((lane >> 4) & 1) + ((q & 3) >> 1), sw = swizzle_v<D>(r);  // the same for r + 8
+  const short* at = v + (16 * kk + r) * D + 8 * ((4 * d + c) ^ sw) + 4 * (q & 1);
+  const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
+  const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D));
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// The outputs' product with V of 16 slots.
+template <int DT, int D>
+__device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, int kk, const s8v& prob) {
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d) w.o[d] = mfma<DT>(operand_v<D>(v, kk, d), prob, w.o[d]);
+}
+
 // ---- own sequences ---------------------------------------------------------
 // The 32 rows of a tile belong to one sequence or to several. Each sequence is
 // taken in tiles of 32 slots by all rows, those of other sequences masked: the
@@ -419,17 +468,20 @@ __device__ __forceinline__ OwnRow own_row(const PrefixDev& p, const Rows& it, in
   return r;
 }
 
-// Whether any of a lane's values is an infinity or NaN.
-template <int DT, int N>
-__device__ __forceinline__ bool any_special(const s8v (&x)[N]) {
+// Whether any of the wave's 32 rows of D values at v holds an infinity or NaN.
+template <int DT, int D>
+__device__ __forceinline__ bool any_special(const short* v) {
   typedef unsigned short us8 __attribute__((ext_vector_type(8)));
-  us8 top = __builtin_bit_cast(us8, x[0]) & (unsigned short)0x7fff;
+  us8 top = {};
 #pragma unroll
-  for (int i = 1; i < N; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(us8, x[i]) & (unsigned short)0x7fff);
-  bool some = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) some |= top[i] >= (DT == EMB_BF16 ? 0x7f80 : 0x7c00);
-  return some;
+  for (int i = 0; i < kPieces<D>; ++i)
+    top = __builtin_elementwise_max(
+        top, *reinterpret_cast<const us8*>(v + 8 * (i * 64 + (threadIdx.x & 63))) & (unsigned short)0x7fff);
+  typedef unsigned short us4 __attribute__((ext_vector_type(4)));
+  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+  const us4 t4 = __builtin_elementwise_max(top.lo, top.hi);
+  const us2 t2 = __builtin_elementwise_max(t4.lo, t4.hi);
+  return __ballot(max(t2.x, t2.y) >= (DT == EMB_BF16 ? 0x7f80 : 0x7c00));
 }
 
 // Tile i of the wave's list.
@@ -464,54 +516,79 @@ __device__ __forceinline__ OwnTile own_look(const PrefixDev& p, const OwnRow& r,
 template <int DT, int D, bool WINDOWS>
 __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, const OwnRow& r, OwnTile next, int h,
                                           int step, short* v) {
+  const int lane = threadIdx.x & 63;
   const KvView& kv = p.a.kv;
   const int total = own_total(r);
-  bool left = false;
-#pragma unroll 1
-  for (int i = 0; i < total; ++i) {
-    OwnTile t = next;
+  const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_short*)v);
+  // a tile's keys into registers, its values into half `buf` of the wave's LDS
+  auto fetch = [&](OwnTile& t, s8v (&kf)[D / 16], int buf) {
     if ((unsigned)t.page >= (unsigned)kv.pages) {
       flag(p, kKvBadPage);
       t.page = 0;
     }
-    s8v kf[D / 16], vr[kPieces<D>];
     load_k<D>(kv, t.page, t.in_page, h, kf);
-    load_v<D>(kv, t.page, t.in_page, h, vr);
-    if (i + 1 < total) next = own_look(p, r, i + 1, step);
-    const bool special = __ballot(any_special<DT>(vr));
+    const uint64_t from = (uint64_t)(kv.v + 2 * (t.page * kv.vps + t.in_page * kv.vss + h * kv.vhs));
+    const int lo = (int)from, hi = (int)(from >> 32);
+#pragma unroll
+    for (int i = 0; i < kPieces<D>; ++i) {
+      const int piece = i * 64 + lane, row = piece / (D / 8), c = piece % (D / 8) ^ swizzle_v<D>(row);
+      const uint64_t at = (uint64_t)(uint32_t)__shfl(hi, row, 64) << 32 | (uint32_t)__shfl(lo, row, 64);
+      fetch16(at + 16 * c, lds + buf * 64 * D + i * 1024);
+    }
+  };
+  bool left = false;
+  OwnTile t = next;
+  s8v kf[D / 16], kn[D / 16];
+  fetch(t, kf, 0);
+  if (total > 1) next = own_look(p, r, 1, step);
+#pragma unroll 1
+  for (int i = 0; i < total; ++i) {
+    short* vt = v + (i & 1) * 32 * D;
+    const OwnTile now = t;
+    f16v s[1] = {};
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) s[0] = mfma<DT>(kf[c], w.q[c], s[0]);
+    wait_fetch();
+    if (i + 1 < total) {
+      t = next;
+      fetch(t, kn, (i + 1) & 1);
+      if (i + 2 < total) next = own_look(p, r, i + 2, step);
+    }
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) kf[c] = kn[c];
+    const bool special = any_special<DT, D>(vt);
     if (special != WINDOWS) {
       left = true;
       continue;
     }
-    f16v s[1] = {};
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) s[0] = mfma<DT>(kf[c], w.q[c], s[0]);
-    const bool mine = r.b == t.b;
-    mask_tile(s[0], t.slot0, mine ? r.seen : 0);
-    if (!WINDOWS) put_v<D>(v, vr, 0, 32);
+    const bool mine = r.b == now.b;
+    mask_tile(s[0], now.slot0, mine ? r.seen : 0);
     s8v prob[2];
     refer<DT, D>(p, w, top_of(s));
     probabilities<DT, D, 1>(p, w, s, prob);
     if (!WINDOWS) {
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) w.o[d] = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], w.o[d]);
+      times_v<DT, D>(w, vt, 0, prob[0]);
+      times_v<DT, D>(w, vt, 1, prob[1]);
       continue;
     }
-    int done = 0;  // limits up to this one are through
-    for (int a = 0; a < 32; ++a) {
+    int done = 1 << 30;  // limits from this one on are through
+    for (int a = 31; a >= 0; --a) {
       const int lim = __builtin_amdgcn_readlane(r.seen, a);
-      if (__builtin_amdgcn_readlane(r.b, a) != t.b || lim <= done) continue;
+      if (__builtin_amdgcn_readlane(r.b, a) != now.b || lim >= done || lim <= now.slot0) continue;
       done = lim;
-      put_v<D>(v, vr, 0, lim - t.slot0);
+#pragma unroll
+      for (int c = 0; c < kPieces<D>; ++c) {
+        const int piece = c * 64 + lane;
+        if (now.slot0 + piece / (D / 8) >= lim) *reinterpret_cast<s8v*>(vt + 8 * piece) = s8v{};
+      }
+      const bool takes = mine && r.seen == lim;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) {
         f16v o = {};
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) o = mfma<DT>(read_vt<D>(v, 16 * kk, 32 * d), prob[kk], o);
+        for (int kk = 0; kk < 2; ++kk) o = mfma<DT>(operand_v<D>(vt, kk, d), prob[kk], o);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) w.o[d][c] += mine && r.seen == lim ? o[c] : 0.f;
+        for (int c = 0; c < 16; ++c) w.o[d][c] += takes ? o[c] : 0.f;
       }
     }
   }
@@ -607,9 +684,11 @@ __device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows
     const int a0 = first_token(p, c0), a1 = first_token(p, c1);
     const int n = lane < p.a.groups && a1 > a0 ? ((a1 - a0) * p.m + rows - 1) / rows : 0;
     int at = 0;  // tiles before this group's
+    const int order = (int)((uint32_t)l >> 5 << 6) + 63 - lane;
+#pragma unroll 4
     for (int j = 0; j < p.a.groups; ++j) {
-      const int lj = __builtin_amdgcn_readlane(l, j), nj = __builtin_amdgcn_readlane(n, j);
-      at += lj > l || (lj == l && j < lane) ? nj : 0;
+      const int nj = __builtin_amdgcn_readlane(n, j);
+      at += __builtin_amdgcn_readlane(order, j) > order ? nj : 0;
     }
     const uint64_t mine = __ballot(tile >= at && tile < at + n);
     if (!mine) return false;
@@ -665,10 +744,10 @@ __device__ __forceinline__ void check_offsets(const PrefixDev& p) {
 template <int DT, int D>
 __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
   constexpr int OS = D + 4;  // row stride of the joined outputs (floats): rows start 4 banks apart
-  constexpr size_t kV = 4 * v_tile_elems<D>() * sizeof(short), kO = (2 * 32 * OS + 4 * 64) * sizeof(float);
+  constexpr size_t kV = 4 * 64 * D * sizeof(short), kO = (2 * 32 * OS + 4 * 64) * sizeof(float);
   __shared__ __attribute__((aligned(16))) char smem[kV > kO ? kV : kO];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  short* v = reinterpret_cast<short*>(smem) + wave * v_tile_elems<D>();
+  short* v = reinterpret_cast<short*>(smem) + wave * 64 * D;
   Wave<DT, D> w;
   check_offsets(p);
   const bool prefix = (int)blockIdx.x < p.prefix_blocks;
@@ -759,31 +838,7 @@ template <int D>
 constexpr int group_slots() {
   return D == 64 ? 8 : 4;
 }
-template <int D>
-__device__ __forceinline__ int swizzle_k(int r) {
-  return D == 128 ? r & 15 : D == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
-}
-template <int D>
-__device__ __forceinline__ int swizzle_v(int r) {
-  return D == 128 ? 4 * (r & 3) : D == 64 ? 2 * (r & 2) : 0;
-}
 
-typedef __attribute__((address_space(3))) short lds_short;
-
-// 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
-// The compiler does not see the transfer: the caller waits (wait_fetch) and
-// passes a barrier before anyone reads. It does not see the instruction's
-// hazards either: a base that a vector instruction wrote would have to be five
-// wait states old, so a scalar one copies it, and that copy is the wait state
-// which m0 needs.
-__device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at) {
-  uint64_t from;
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
-               : "=&s"(from)
-               : "s"(at), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-__device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 // A wave's fetches of 32 slots ("half" a tile): kH groups of kGroup slots. Lane l
 // holds the addresses of group l % kH of half l / kH - 1 of a window of 64 / kH
@@ -793,7 +848,7 @@ struct Fetch {
   static constexpr int kGroup = group_slots<D>();
   static constexpr int kH = 32 / (NW * kGroup);
   static constexpr int kPairs = 32 / kH;  // of halves, in a window
-  static_assert(kH >= 1 && NW * kGroup % 16 == 0, "every group of a wave swizzles alike");
+  static_assert(NW == 4 && kH >= 1 && NW * kGroup % 16 == 0, "every group of a wave swizzles alike");
   struct Half {
     uint64_t k[kH], v[kH];  // uniform: where its groups' rows are
   };
@@ -874,21 +929,6 @@ __device__ __forceinline__ void read_k(const short* k, s8v (&kf)[D / 16]) {
   for (int i = 0; i < D / 16; ++i) kf[i] = *reinterpret_cast<const s8v*>(k + r * D + 8 * ((2 * i) ^ sw));
 }
 
-// The outputs' product with V (rows of LDS at v) of 16 slots.
-template <int DT, int D>
-__device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, int kk, const s8v& prob) {
-  const int lane = threadIdx.x & 63, q = lane & 15;
-  const int r = 4 * (lane >> 5) + (q >> 2);
-  const int c = 2 * ((lane >> 4) & 1) + ((q & 3) >> 1), sw = swizzle_v<D>(r);  // the same for r + 8
-#pragma unroll
-  for (int d = 0; d < D / 32; ++d) {
-    const short* at = v + (16 * kk + r) * D + 8 * ((4 * d + c) ^ sw) + 4 * (q & 1);
-    const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)at);
-    const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D));
-    w.o[d] = mfma<DT>(__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7), prob, w.o[d]);
-  }
-}
-
 // 32 slots: their scores `s` (maximum `top`) become probabilities and meet V,
 // while the matrix units make the next 32 slots' scores `t` of the keys kf. One
 // stream of instructions in which every product is followed by the vector
@@ -927,8 +967,7 @@ template <int DT, int D, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   using F = Fetch<D, NW>;
   constexpr int kRows = kTile * D;  // elements of a tile
-  constexpr int kWide = 4 * kRows, kOwn = NW * v_tile_elems<D>();
-  __shared__ __attribute__((aligned(1024))) short smem[kWide > kOwn ? kWide : kOwn];
+  __shared__ __attribute__((aligned(1024))) short smem[4 * kRows];  // own tiles: 64 rows for each wave
   __shared__ OwnRow s_own[NW][32];
   __shared__ int s_page[NW][32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -953,7 +992,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   if (prefix) it.r0 += 32 * wave;
   const bool live = it.r0 < it.rows;  // waves without rows only fetch
   Wave<DT, D> w;
-  load_q<DT, D>(p, it, w);
   const bool some = x.k0 < k1, own = live && (!prefix || p.nos == 0);
   const int own_step = prefix ? p.nps : p.nos;
   F f;
@@ -963,8 +1001,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   // 32 slots' places: K 0 to 3 (two tiles), V 4 to 7
   auto fetch_k = [&](const typename F::Half& h, int place) { f.rows(h.k, f.koff, lds + kRows * place); };
   auto fetch_v = [&](const typename F::Half& h, int place) { f.rows(h.v, f.voff, lds + kRows * place); };
+  if (some) f.look(p, x.pages, x.k0, k1);
+  load_q<DT, D>(p, it, w);
   if (some) {
-    f.look(p, x.pages, x.k0, k1);
     f.turn_to_next(p, it.h);
     f.take(p, x.pages, it.h, x.k0, k1, &ha, &hb);
     fetch_k(hb, 2);
@@ -1038,7 +1077,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   if (!live) return;
   if (own)
     own_slots<DT, D>(p, w, s_own[wave][threadIdx.x & 31], s_page[wave][threadIdx.x & 31], it.h, own_step,
-                     smem + wave * v_tile_elems<D>());
+                     smem + wave * 64 * D);
   store_rows<DT, D>(p, it, w, prefix ? part : p.nps + part);
 }
 
