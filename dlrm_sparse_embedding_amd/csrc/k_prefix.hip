@@ -170,17 +170,18 @@ __device__ __forceinline__ void load_q(const PrefixDev& p, const Rows& it, Wave<
   w.sum = 0.f;
 }
 
-// Row (page, slot) of a slot's keys and values; a slot without a page reads
-// page 0 and raises the flag (its values are then meaningless, but in range).
-__device__ __forceinline__ void locate(const PrefixDev& p, const int* pages, int slot, int* page, int* in_page) {
+// Slot `slot` of a page table row, without a check of the page.
+__device__ __forceinline__ int page_of(const PrefixDev& p, const int* pages, int slot, int* in_page) {
   const int col = div_by(p.a.kv.by_page, slot);
-  int pg = pages[col];
-  if (pg < 0 || pg >= p.a.kv.pages) {
-    flag(p, kKvBadPage);
-    pg = 0;
-  }
-  *page = pg;
   *in_page = slot - col * p.a.kv.page;
+  return pages[col];
+}
+// A slot without a page reads page 0 and raises the flag (its values are then
+// meaningless, but in range).
+__device__ __forceinline__ int checked(const PrefixDev& p, int page) {
+  if ((unsigned)page < (unsigned)p.a.kv.pages) return page;
+  flag(p, kKvBadPage);
+  return 0;
 }
 
 // Elements between rows of a wave's own V tile: 4 rows, 64 bytes of each, are
@@ -298,19 +299,21 @@ __device__ __forceinline__ void put_v(short* v, const s8v (&vr)[kPieces<D>], int
 
 // One wave over the prefix slots k0, k0 + step, .. below k1 in tiles of 32, the
 // keys straight into registers (each is used once) and the values through the
-// wave's own LDS tile.
+// wave's own LDS tile. next_page, next_in: the first tile's, from first_page.
+__device__ __forceinline__ int first_page(const PrefixDev& p, const int* pages, int k, int k1, int* in_page) {
+  // slots past the end read the last one again; their scores are masked
+  return page_of(p, pages, min(k + (int)(threadIdx.x & 31), k1 - 1), in_page);
+}
 template <int DT, int D>
 __device__ void wave_slots(const PrefixDev& p, Wave<DT, D>& w, const int* pages, int h, int k0, int k1, int step,
-                           short* v) {
-  const int lane = threadIdx.x & 63;
+                           short* v, int next_page, int next_in) {
 #pragma unroll 1
   for (int k = k0; k < k1; k += step) {
-    int page, in_page;
-    // slots past the end read the last one again; their scores are masked
-    locate(p, pages, min(k + (lane & 31), k1 - 1), &page, &in_page);
+    const int page = checked(p, next_page), in_page = next_in;
     s8v kf[D / 16], vr[kPieces<D>];
     load_k<D>(p.a.kv, page, in_page, h, kf);
     load_v<D>(p.a.kv, page, in_page, h, vr);
+    if (k + step < k1) next_page = first_page(p, pages, k + step, k1, &next_in);
     f16v s[1] = {};
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(kf[i], w.q[i], s[0]);
@@ -522,10 +525,7 @@ __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, co
   const uint32_t lds = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_short*)v);
   // a tile's keys into registers, its values into half `buf` of the wave's LDS
   auto fetch = [&](OwnTile& t, s8v (&kf)[D / 16], int buf) {
-    if ((unsigned)t.page >= (unsigned)kv.pages) {
-      flag(p, kKvBadPage);
-      t.page = 0;
-    }
+    t.page = checked(p, t.page);
     load_k<D>(kv, t.page, t.in_page, h, kf);
     const uint64_t from = (uint64_t)(kv.v + 2 * (t.page * kv.vps + t.in_page * kv.vss + h * kv.vhs));
     const int lo = (int)from, hi = (int)(from >> 32);
@@ -761,6 +761,10 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
     x.s1 = p.a.seqs;
   }
   const Rows it = x.it;
+  const int k0 = prefix ? x.k0 + 32 * wave : 0, k1 = prefix ? x.k1 : 0;
+  // what the first prefix tile and the own slots need is looked up at once
+  int first = 0, first_in = 0;
+  if (k0 < k1) first = first_page(p, x.pages, k0, k1, &first_in);
   load_q<DT, D>(p, it, w);
   const bool own = !prefix || p.nos == 0;
   const int step = prefix ? p.nps * 4 : p.nos;
@@ -770,7 +774,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
     r = own_row(p, it, x.s0, x.s1, prefix ? part * 4 + wave : part, step);
     if (own_total(r) > 0) page = own_look(p, r, 0, step).page;
   }
-  if (prefix) wave_slots<DT, D>(p, w, x.pages, it.h, x.k0 + 32 * wave, x.k1, 128, v);
+  if (prefix) wave_slots<DT, D>(p, w, x.pages, it.h, k0, k1, 128, v, first, first_in);
   if (own) own_slots<DT, D>(p, w, r, page, it.h, step, v);
   if (prefix) {
     // join: waves 2 and 3 into 0 and 1, then 1 into 0
@@ -876,16 +880,11 @@ struct Fetch {
     const int l = threadIdx.x & 63;
     const long long at = k0 + (2 * kPairs * (long long)window + l / kH - 1) * 32 + (l % kH * NW + wave) * kGroup;
     const int slot = (int)min(max(at, (long long)k0), (long long)((k1 - 1) / kGroup * kGroup));
-    const int col = div_by(p.a.kv.by_page, slot);
-    page = table[col];
-    in_page = slot - col * p.a.kv.page;
+    page = page_of(p, table, slot, &in_page);
   }
   __device__ __forceinline__ void turn_to_next(const PrefixDev& p, int h) {
     const KvView& kv = p.a.kv;
-    if ((unsigned)page >= (unsigned)kv.pages) {
-      flag(p, kKvBadPage);
-      page = 0;
-    }
+    page = checked(p, page);
     k = (uint64_t)(kv.k + 2 * (page * kv.kps + in_page * kv.kss + h * kv.khs));
     v = (uint64_t)(kv.v + 2 * (page * kv.vps + in_page * kv.vss + h * kv.vhs));
   }
@@ -930,14 +929,17 @@ __device__ __forceinline__ void read_k(const short* k, s8v (&kf)[D / 16]) {
 }
 
 // 32 slots: their scores `s` (maximum `top`) become probabilities and meet V,
-// while the matrix units make the next 32 slots' scores `t` of the keys kf. One
-// stream of instructions in which every product is followed by the vector
-// work of about its own time; left to itself the compiler puts the LDS reads
-// right before their use and waits for each. NEXT: kf then takes the keys at k.
+// while the matrix units make the next 32 slots' scores `t` of the keys kf. NEXT:
+// kf then takes the keys at k. The wave goes first on its SIMD from the first
+// product to the last, so that the two waves there take turns with products and
+// scalar work instead of mixing them (1024 candidates over 32768 slots 600 ->
+// 572 us; sequences given with sched_group_barrier measured the same as the
+// compiler's own).
 template <int DT, int D, bool NEXT>
 __device__ __forceinline__ void half_step(const PrefixDev& p, Wave<DT, D>& w, f16v (&s)[1], f16v (&t)[1], float& top,
                                           s8v (&kf)[D / 16], const short* v, const short* k) {
   refer<DT, D>(p, w, top);
+  __builtin_amdgcn_s_setprio(1);
   t[0] = f16v{};
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) t[0] = mfma<DT>(kf[i], w.q[i], t[0]);
@@ -946,21 +948,8 @@ __device__ __forceinline__ void half_step(const PrefixDev& p, Wave<DT, D>& w, f1
   times_v<DT, D>(w, v, 0, prob[0]);
   if (NEXT) read_k<D>(k, kf);
   times_v<DT, D>(w, v, 1, prob[1]);
+  __builtin_amdgcn_s_setprio(0);
   top = top_of(t);
-  constexpr int kMfma = 0x8, kValu = 0x2, kLds = 0x100;
-  __builtin_amdgcn_sched_group_barrier(kLds, D / 16, 0);  // V of slots 0 .. 15
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    if (i >= D / 32) __builtin_amdgcn_sched_group_barrier(kLds, 2, 0);  // and of 16 .. 31
-    __builtin_amdgcn_sched_group_barrier(kValu, 640 / D, 0);
-  }
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-    if (NEXT && i < D / 32) __builtin_amdgcn_sched_group_barrier(kLds, 2, 0);
-    __builtin_amdgcn_sched_group_barrier(kValu, 6, 0);
-  }
 }
 
 template <int DT, int D, int NW>
