@@ -725,3 +725,93 @@ def test_pages_beyond_32_bits():
     shift = lambda t: t - first
     check_attention(out, lse, q, kc[first:], vc[first:], 0.1, [0, 1], [10], shift(table),
                     (i32([0, 1]), i32([100]), shift(pt)), "bf16")
+
+
+# ---- attention: blocks that take several groups', sequences' and parts' work --------------
+
+def test_attention_many_groups_and_empty_sequences():
+    # more groups than a wave has lanes, runs of more sequences without tokens than that between two
+    # with some, groups of such sequences alone, groups without sequences
+    rng = np.random.default_rng(61)
+    counts = []
+    for i in range(12):
+        counts += [int(n) for n in rng.integers(1, 6, 3)] + [0] * int(rng.choice([0, 1, 70, 130]))
+    cuts = np.sort(rng.choice(len(counts) + 1, 79, replace=True))
+    sizes = np.diff(np.concatenate([[0], cuts, [len(counts)]]))
+    lens = [c + int(n) if c else int(n) for c, n in zip(counts, rng.integers(0, 40, len(counts)))]
+    prefix = [int(n) for n in rng.integers(0, 50, len(sizes))]
+    for hq, hk in ((4, 2), (2, 2)):
+        q, kc, vc, off, lens_, table, groups = attention_case("bf16", 64, hq, hk, 16, counts, lens, sizes, prefix)
+        cache = E.KVCache(kc, vc)
+        out, lse = run_attention(cache, q, 0.125, i32(off), i32(lens), table, groups)
+        cache.check_error()
+        check_attention(out, lse, q, kc, vc, 0.125, off, lens, table, groups, "bf16")
+        # the same sequences without prefixes
+        out, lse = run_attention(cache, q, 0.125, i32(off), i32(lens), table)
+        cache.check_error()
+        check_attention(out, lse, q, kc, vc, 0.125, off, lens, table, None, "bf16")
+        # in one group: a long run of empty sequences inside a tile of rows
+        one = (i32([0, len(counts)]), groups[1][:1].contiguous(), groups[2][:1].contiguous())
+        out, lse = run_attention(cache, q, 0.125, i32(off), i32(lens), table, one)
+        cache.check_error()
+        check_attention(out, lse, q, kc, vc, 0.125, off, lens, table, one, "bf16")
+
+
+# (counts, lens, group sizes, prefixes, pages of table width to add): rows enough for tiles of 128 with the
+# own slots taken along, parts of a prefix with them, own slots in blocks of their own (a wide table)
+SHARED = {
+    "tiles": ([1, 2] * 60, [20] * 60 + [33] * 60, [70, 50], [40, 333], 0),
+    "parts": ([1, 3] * 40, [5, 40] * 40, [80], [1500], 0),
+    "wide_table": ([1, 2] * 60, [20] * 60 + [33] * 60, [70, 50], [40, 333], 30),
+    "no_prefix": ([1, 2] * 20, [20] * 20 + [33] * 20, [], [], 0),
+}
+
+
+@pytest.mark.parametrize("dt,D", [("bf16", 128), ("f16", 64), ("bf16", 96)])
+@pytest.mark.parametrize("kind", list(SHARED))
+def test_attention_rows_do_not_touch_each_other(dt, D, kind):
+    counts, lens, gs, prefix, more = SHARED[kind]
+    q, kc, vc, off, lens, table, groups = attention_case(dt, D, 4, 2, 16, counts, lens, gs, prefix)
+    table = torch.cat([table, torch.full((len(lens), more), -1, dtype=torch.int32, device="cuda")], 1)
+    cache = E.KVCache(kc, vc)
+    base, base_l = run_attention(cache, q, 0.125, i32(off), i32(lens), table, groups)
+    cache.check_error()
+    check_attention(base, base_l, q, kc, vc, 0.125, off, lens, table, groups, dt)
+    # sequence 7's own slots hold infinities, NaN and huge keys: only its rows may notice
+    own = [int(x) for x in table[7][:-(-lens[7] // 16)]]
+    t0, t1 = int(off[7]), int(off[8])
+    rest = torch.ones(q.shape[0], dtype=torch.bool, device="cuda")
+    rest[t0:t1] = False
+    k1, v1 = kc.clone(), vc.clone()
+    for poison in (float("nan"), float("inf"), torch.finfo(DT[dt]).max):
+        kc[own], vc[own] = poison, poison
+        got, got_l = run_attention(cache, q, 0.125, i32(off), i32(lens), table, groups)
+        assert torch.equal(got[rest], base[rest]) and torch.equal(got_l[rest], base_l[rest]), poison
+        kc.copy_(k1), vc.copy_(v1)
+    # an infinite value that only its last query sees: that row alone changes, and to an infinity
+    if counts[7] > 1:
+        pg, sl = int(table[7][(lens[7] - 1) // 16]), (lens[7] - 1) % 16
+        vc[pg, sl] = float("inf")
+        got, got_l = run_attention(cache, q, 0.125, i32(off), i32(lens), table, groups)
+        rest[t0:t1 - 1] = True
+        assert torch.equal(got[rest], base[rest]) and torch.equal(got_l, base_l)
+        assert torch.isposinf(got[t1 - 1]).all()
+        vc.copy_(v1)
+    # and its length is its own matter too
+    other = list(lens)
+    other[7] = counts[7]
+    got, got_l = run_attention(cache, q, 0.125, i32(off), i32(other), table, groups)
+    rest[t0:t1] = False
+    assert torch.equal(got[rest], base[rest]) and torch.equal(got_l[rest], base_l[rest])
+
+
+def test_attention_direct_result_in_strides_and_order_of_groups():
+    # one part: the result is written by the prefix' blocks; the groups' order is not the lengths'
+    case = ("bf16", 128, 8, 2, 16, [2] * 90, [7] * 90, [20, 50, 20], [100, 20, 240])
+    q, kc, vc, off, lens, table, groups = attention_case(*case)
+    cache = E.KVCache(kc, vc)
+    out = torch.full((180, 8, 256), 5.0, dtype=q.dtype, device="cuda")
+    got, lse = run_attention(cache, q, -0.3, i32(off), i32(lens), table, groups, out=out[..., 128:])
+    cache.check_error()
+    check_attention(got, lse, q, kc, vc, -0.3, off, lens, table, groups, "bf16")
+    assert (out[..., :128] == 5.0).all()
