@@ -5,4 +5,4 @@ The compute path is the HIP library ``libemb.so`` (C ABI in ``include/emb.h``);
 package loads nothing: the binding loads the library on first use and raises if
 it is missing.
 """
-__all__ = ["workloads", "emb"]
+__all__ = ["workloads", "emb", "ranking"]
