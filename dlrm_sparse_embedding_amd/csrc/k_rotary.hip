@@ -240,30 +240,37 @@ __global__ __launch_bounds__(256) void k_norm_rotary_back_any(NormRotaryBackArgs
 }
 
 // Weights' gradients from the blocks' partial sums, in 64 bits: 4 columns for
-// each block, 64 lanes down the blocks for each column.
+// each block, a row of them for each thread, so that (with up to 1280 rows) all
+// loads are under way at once.
 __global__ __launch_bounds__(256) void k_norm_dw(const float* __restrict__ part, int blocks, int dim,
                                                  float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ double s[256];
-  const int col = blockIdx.x * 4 + (threadIdx.x & 3);
-  const int row = threadIdx.x >> 2;
-  double acc = 0.0;
-  if (col < 2 * dim)
-    for (int b = row; b < blocks; b += 8 * 64) {
-      float x[8];
+  __shared__ double s[4][256];
+  const int col = blockIdx.x * 4;
+  double acc[4] = {0.0, 0.0, 0.0, 0.0};
+  for (int b0 = threadIdx.x; b0 < blocks; b0 += 5 * 256) {
+    float x[5][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = b + 64 * i < blocks ? part[(long long)(b + 64 * i) * 2 * dim + col] : 0.f;
+    for (int i = 0; i < 5; ++i)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc += (double)x[i];
-    }
-  s[threadIdx.x] = acc;
-  __syncthreads();
-  for (int d = 32; d >= 1; d >>= 1) {
-    if (row < d) s[threadIdx.x] += s[threadIdx.x + 4 * d];
-    __syncthreads();
+      for (int c = 0; c < 4; ++c) {
+        const int b = b0 + 256 * i;
+        x[i][c] = b < blocks && col + c < 2 * dim ? part[(long long)b * 2 * dim + col + c] : 0.f;
+      }
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] += (double)x[i][c];
   }
-  if (row == 0 && col < 2 * dim) {
-    float* out = col < dim ? dwq : dwk;
-    if (out) out[col < dim ? col : col - dim] = (float)s[threadIdx.x];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) s[c][threadIdx.x] = acc[c];
+  __syncthreads();
+  // a wave for each column
+  const int c = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  double sum = s[c][lane] + s[c][lane + 64] + s[c][lane + 128] + s[c][lane + 192];
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_down(sum, d, 64);
+  if (lane == 0 && col + c < 2 * dim) {
+    float* out = col + c < dim ? dwq : dwk;
+    if (out) out[col + c < dim ? col + c : col + c - dim] = (float)sum;
   }
 }
 
