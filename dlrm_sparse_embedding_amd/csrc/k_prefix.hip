@@ -365,6 +365,8 @@ __device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at
                : "memory", "m0");
 }
 __device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// Before a wave fetches into LDS that it has read itself: its reads are over.
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // The same with an address for each lane.
 __device__ __forceinline__ void fetch16(uint64_t from, uint32_t at) {
@@ -395,9 +397,9 @@ __device__ __forceinline__ void times_v(Wave<DT, D>& w, const short* v, int kk, 
 
 // ---- own sequences ---------------------------------------------------------
 // The 32 rows of a tile belong to one sequence or to several. Each sequence is
-// taken in tiles of 32 slots by all rows, those of other sequences masked: the
-// matrix units idle less than the memory system needs anyway. The sequences'
-// tiles form one list, so that the next tile's page is looked up while this one
+// taken in tiles of 32 slots by all rows, those of other sequences masked: such
+// tiles wait for their reads, and products of masked rows cost nothing on top.
+// The sequences' tiles form one list, so that the next tile's page is looked up while this one
 // is worked on. With several waves to share it, tile t of sequence b goes to
 // wave (b + t) % step: where a sequence is cut does not depend on its
 // neighbours, and neither does a bit of its result.
@@ -546,6 +548,7 @@ __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, co
   bool left = false;
   OwnTile t = next;
   s8v kf[D / 16], kn[D / 16];
+  wait_reads();
   fetch(t, kf, 0);
   if (total > 1) next = own_look(p, r, 1, step);
 #pragma unroll 1
@@ -558,6 +561,7 @@ __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, co
     wait_fetch();
     if (i + 1 < total) {
       t = next;
+      wait_reads();
       fetch(t, kn, (i + 1) & 1);
       if (i + 2 < total) next = own_look(p, r, i + 2, step);
     }
@@ -842,7 +846,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
 //
 // A wave fetches whole slots' rows, kGroup at a time; with pages of a multiple
 // of kGroup slots they lie in one page. The lanes look up the pages of the
-// wave's next 64 groups at once; the addresses are scalar arithmetic.
+// wave's next 64 groups at once and hold their addresses for the fetches.
 constexpr int kTile = 64;
 
 template <int D>
