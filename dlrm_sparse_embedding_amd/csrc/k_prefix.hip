@@ -356,13 +356,14 @@ typedef __attribute__((address_space(3))) short lds_short;
 // passes a barrier before anyone reads. It does not see the instruction's
 // hazards either: a base that a vector instruction wrote would have to be five
 // wait states old, so a scalar one copies it, and that copy is the wait state
-// which m0 needs.
+// which m0 needs. (m0 has no other user here: LDS accesses need none on this
+// architecture, and no register is indexed.)
 __device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at) {
   uint64_t from;
   asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
                : "=&s"(from)
                : "s"(at), "v"(off), "s"(base)
-               : "memory", "m0");
+               : "memory");
 }
 __device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // Before a wave fetches into LDS that it has read itself: its reads are over.
@@ -373,7 +374,7 @@ __device__ __forceinline__ void fetch16(uint64_t from, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(at), "v"(from)
-               : "memory", "m0");
+               : "memory");
 }
 
 // V^T operand of 16 slots from slot 16 kk and 32 columns from 32 d (rows of LDS at v).
@@ -696,7 +697,6 @@ __device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows
     const int n = lane < p.a.groups && a1 > a0 ? ((a1 - a0) * p.m + rows - 1) / rows : 0;
     int at = 0;  // tiles before this group's
     const int order = (int)((uint32_t)l >> 5 << 6) + 63 - lane;
-#pragma unroll 4
     for (int j = 0; j < p.a.groups; ++j) {
       const int nj = __builtin_amdgcn_readlane(n, j);
       at += __builtin_amdgcn_readlane(order, j) > order ? nj : 0;
@@ -986,7 +986,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
     x.k0 = x.k1 = 0;
   }
   const int k1 = x.k1;
-  const KvView& kv = p.a.kv;
   Rows it = x.it;
   it.h = __builtin_amdgcn_readfirstlane(it.h);
   if (prefix) it.r0 += 32 * wave;
