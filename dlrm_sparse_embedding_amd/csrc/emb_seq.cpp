@@ -117,7 +117,7 @@ int norm_rotary_back_blocks(long long tokens, int hq, int hk, int dim) {
 //
 // Short own sequences are taken by the blocks of their rows' prefix, spread over
 // its parts: with one part the result is written directly, without partial
-// outputs (24 users' 1200 candidates: 142 -> 128 us). Beyond kOwnInPrefix slots
+// outputs (24 users' 1200 candidates: 142 -> 125 us). Beyond kOwnInPrefix slots
 // of table width they would hold these blocks up, and get blocks of their own.
 constexpr long long kOwnInPrefix = 256;
 
