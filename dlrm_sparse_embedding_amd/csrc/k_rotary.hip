@@ -552,11 +552,12 @@ __device__ __forceinline__ bool place(const AppendArgs& a, int t, int* page, int
   if (a.offsets) {
     b = seq_of(a.offsets, a.seqs, t);
     first = a.offsets[b];
-    n = a.offsets[b + 1] - first;
-    if (t < first || t >= first + n) {  // offsets that do not cover the token
+    const int next = a.offsets[b + 1];
+    if (first < 0 || t < first || t >= next || next > a.tokens) {  // offsets that do not cover the token, or more
       if (a.kv.error) atomicOr(a.kv.error, kKvBadOffsets);
       return false;
     }
+    n = next - first;
   }
   const long long s = (long long)a.lens[b] - n + (t - first);
   if (s < 0 || s >= (long long)a.width * a.kv.page) {
@@ -579,6 +580,7 @@ template <int DT>
 __global__ __launch_bounds__(256) void k_append_any(AppendArgs a, RotTable rot) {
   const int H = 2 * a.kv.heads;
   const KvView& kv = a.kv;
+  if (a.offsets) report_offsets(a.offsets, a.seqs, (int)a.tokens, kv.error);
   for (long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 6); item < a.tokens * H;
        item += (long long)gridDim.x * 4) {
     const long long t = item / H;
@@ -608,6 +610,7 @@ __global__ __launch_bounds__(256, 4) void k_append_vec(AppendArgs a, VecShape sh
   const bool busy = u < sh.units;
   Unit<DT, LAYOUT> un;
   un.place(u, rot);
+  if (a.offsets) report_offsets(a.offsets, a.seqs, (int)a.tokens, kv.error);
   for (long long item = (long long)blockIdx.x * per + threadIdx.x / sh.G; item < sh.items;
        item += (long long)gridDim.x * per) {
     const int t = (int)(((uint64_t)(uint32_t)item * sh.by_g.mul) >> sh.by_g.shift);

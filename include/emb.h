@@ -605,7 +605,9 @@ int emb_check_kv_error(emb_kv* kv, void* hip_stream);
  * NULL, by positions[token] (of itype) or, where positions is NULL, by the
  * slot. Values are copied. A token whose slot has no page (a negative slot,
  * one beyond the table's width, a page outside [0, pages)) is not stored and
- * raises the error flag. Two tokens of one call must not share a slot. */
+ * raises the error flag. Offsets that break their contract anywhere raise it
+ * too; a sequence whose offsets leave [0, tokens] is then not stored, others go
+ * to slots of their own tables or nowhere. Two tokens of one call must not share a slot. */
 int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dtype, int32_t heads, int32_t dim,
                   const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
                   const int32_t* offsets, int32_t seqs, const int32_t* lens, const int32_t* table,
