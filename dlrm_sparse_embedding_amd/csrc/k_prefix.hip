@@ -742,12 +742,10 @@ __device__ __forceinline__ bool own_item(const PrefixDev& p, int block, Rows* it
   return h < p.a.kv.heads;
 }
 
-// One thread's look at the offsets' ends.
+// Reports offsets that break their contract. Their look at every pair is spread over the grid.
 __device__ __forceinline__ void check_offsets(const PrefixDev& p) {
-  if (blockIdx.x != 0 || threadIdx.x != 0) return;
-  if (p.a.offsets && (p.a.offsets[0] != 0 || p.a.offsets[p.a.seqs] != p.a.tokens)) flag(p, kKvBadOffsets);
-  if (p.a.groups > 0 && (p.a.group_offsets[0] != 0 || p.a.group_offsets[p.a.groups] != p.a.seqs))
-    flag(p, kKvBadOffsets);
+  if (p.a.offsets) report_offsets(p.a.offsets, p.a.seqs, p.a.tokens, p.a.kv.error);
+  if (p.a.groups > 0) report_offsets(p.a.group_offsets, p.a.groups, p.a.seqs, p.a.kv.error);
 }
 
 // Few rows: a block takes one tile of 32 rows, a cache head and a part of the

@@ -634,6 +634,8 @@ int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dty
  * aligned and their strides multiples of 16 bytes; EMB_E_INVAL otherwise
  * (EMB_E_DTYPE for an fp32 cache). Softmax statistics and sums are fp32; the
  * probabilities are rounded to the cache's type for the matrix product.
+ * Offsets and group offsets that break their contract anywhere raise the
+ * cache's error flag; the call's results are then unspecified.
  * ws: device, 16-byte aligned, at least
  * emb_prefix_attention_workspace_bytes (0 on invalid arguments). */
 size_t emb_prefix_attention_workspace_bytes(const emb_kv* kv, int64_t tokens, int32_t q_heads, int32_t groups,

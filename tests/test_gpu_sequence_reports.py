@@ -1,8 +1,6 @@
 """GPU tests of what calls on a paged cache report: offsets that break their contract inside as well as at
 their ends, and lengths that a page table does not hold. Every input here stays inside the buffers, and no two
 tokens of an append meet in a slot."""
-import math
-
 import pytest
 import torch
 
@@ -70,3 +68,61 @@ def test_append_reports_no_good_offsets(dt, D):
     off[680] = 1               # far behind the last token
     E.emb_kv_append(cache.handle, None, k, v, i32(off), lens, table)
     assert reported(cache) == E.EMB_E_INVAL
+
+
+# ---- the attention -------------------------------------------------------------------------
+# 8 tokens: with 2 query heads of a cache head 16 rows, in tiles of 32 (narrow), with 32 of them 256 rows, in
+# tiles of 128 that share their keys (wide)
+
+KERNELS = {"narrow": (4, 2), "wide": (64, 2)}
+
+
+def attention(hq, hk, off, groups=None, counts=(3, 2, 3), lens=(9, 40, 5), prefix=(70,)):
+    q, kc, vc, _, _, table, good = attention_case("bf16", 64, hq, hk, 16, list(counts), list(lens), [len(lens)], list(prefix))
+    cache = E.KVCache(kc, vc)
+    run_attention(cache, q, 0.125, i32(off), i32(lens), table, groups(good) if groups else None)
+    return reported(cache)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("own_blocks", [False, True])
+@pytest.mark.parametrize("off,code", [
+    ([0, 3, 5, 8], 0),
+    ([0, 5, 3, 8], E.EMB_E_INVAL),             # decreasing inside
+    ([0, 3, 2147483647, 8], E.EMB_E_INVAL),
+    ([0, -1, 5, 8], E.EMB_E_INVAL),
+    ([0, 3, 5, 9], E.EMB_E_INVAL),
+    ([1, 3, 5, 8], E.EMB_E_INVAL),
+])
+def test_attention_reports_offsets(kernel, own_blocks, off, code):
+    hq, hk = KERNELS[kernel]
+    assert attention(hq, hk, off, groups=None if own_blocks else lambda good: good) == code
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_attention_reports_offsets_of_groups(kernel):
+    hq, hk = KERNELS[kernel]
+    _, pl, pt = attention_case("bf16", 64, hq, hk, 16, [3, 2, 3], [9, 40, 5], [3], [70])[6]
+    run = lambda go: attention(hq, hk, [0, 3, 5, 8], groups=lambda good: (
+        i32(go), pl.repeat(len(go) - 1), pt.repeat(len(go) - 1, 1)))
+    assert run([0, 1, 1, 3]) == 0
+    # decreasing inside; beyond the sequences, where they are cut, so no two groups share a row
+    assert run([0, 5, 3]) == E.EMB_E_INVAL
+    assert run([0, 5, 4, 3]) == E.EMB_E_INVAL
+    assert run([0, -1, 3]) == E.EMB_E_INVAL
+
+
+def test_attention_reports_offsets_of_many_groups():
+    # more groups than a wave has lanes, and than a block has threads
+    hq, hk = 4, 2
+    counts, lens = [1] * 400, [3] * 400
+    q, kc, vc, _, _, table, _ = attention_case("bf16", 64, hq, hk, 16, counts, lens, [400], [40])
+    cache = E.KVCache(kc, vc)
+    pages = torch.arange(3, dtype=torch.int32, device="cuda")[None].repeat(400, 1)
+    good = list(range(401))
+    beyond = good[:300] + [400] * 101
+    beyond[350] = 450                     # cut to the sequences: no group shares a row
+    last = good[:399] + [407, 400]
+    for go, code in ((good, 0), (beyond, E.EMB_E_INVAL), (last, E.EMB_E_INVAL)):
+        run_attention(cache, q, 0.125, None, i32(lens), table, (i32(go), i32([40] * 400), pages))
+        assert reported(cache) == code
