@@ -681,17 +681,13 @@ __device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows
   const int h = id / p.nps;
   if (h >= p.a.kv.heads) return false;  // the grid is a multiple of 8
   const long long cap = (long long)p.a.pwidth * p.a.kv.page;
-  auto limit = [&](int n, bool report) {
-    if (n >= 0 && n <= cap) return n;
-    if (report) flag(p, kKvBadPage);
-    return n < 0 ? 0 : (int)cap;
-  };
+  auto limit = [&](int n) { return n < 0 ? 0 : (int)min((long long)n, cap); };  // check_sequences reports others
   int g, t0, t1, len;
   if (p.a.groups <= 64) {
     // A group for each lane; tiles in the order of falling prefix lengths, so
     // that the longest are not the last to start.
     const int lane = threadIdx.x & 63, i = min(lane, p.a.groups - 1);
-    const int l = limit(p.a.prefix_lens[i], threadIdx.x < 64 && (int)threadIdx.x < p.a.groups);
+    const int l = limit(p.a.prefix_lens[i]);
     const int c0 = min(max(p.a.group_offsets[i], 0), p.a.seqs), c1 = min(max(p.a.group_offsets[i + 1], 0), p.a.seqs);
     const int a0 = first_token(p, c0), a1 = first_token(p, c1);
     const int n = lane < p.a.groups && a1 > a0 ? ((a1 - a0) * p.m + rows - 1) / rows : 0;
@@ -718,7 +714,7 @@ __device__ __forceinline__ bool prefix_item(const PrefixDev& p, int id, int rows
     t1 = group_token(p, g + 1);
     w->it = Rows{t0, (tile - (g + t0 * p.m / rows)) * rows, (t1 - t0) * p.m, h};
     if (w->it.r0 < 0 || w->it.r0 >= w->it.rows) return false;
-    len = limit(p.a.prefix_lens[g], threadIdx.x == 0);
+    len = limit(p.a.prefix_lens[g]);
     w->s0 = min(max(p.a.group_offsets[g], 0), p.a.seqs);
     w->s1 = min(max(p.a.group_offsets[g + 1], 0), p.a.seqs);
   }
@@ -742,10 +738,15 @@ __device__ __forceinline__ bool own_item(const PrefixDev& p, int block, Rows* it
   return h < p.a.kv.heads;
 }
 
-// Reports offsets that break their contract. Their look at every pair is spread over the grid.
-__device__ __forceinline__ void check_offsets(const PrefixDev& p) {
+// Reports offsets that break their contract and prefixes that their tables do
+// not hold, spread over the grid.
+__device__ __forceinline__ void check_sequences(const PrefixDev& p) {
   if (p.a.offsets) report_offsets(p.a.offsets, p.a.seqs, p.a.tokens, p.a.kv.error);
-  if (p.a.groups > 0) report_offsets(p.a.group_offsets, p.a.groups, p.a.seqs, p.a.kv.error);
+  if (p.a.groups == 0) return;
+  report_offsets(p.a.group_offsets, p.a.groups, p.a.seqs, p.a.kv.error);
+  const long long cap = (long long)p.a.pwidth * p.a.kv.page;
+  for (long long g = (long long)blockIdx.x * 256 + threadIdx.x; g < p.a.groups; g += (long long)gridDim.x * 256)
+    if (p.a.prefix_lens[g] < 0 || p.a.prefix_lens[g] > cap) flag(p, kKvBadPage);
 }
 
 // Few rows: a block takes one tile of 32 rows, a cache head and a part of the
@@ -758,7 +759,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(PrefixDev p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   short* v = reinterpret_cast<short*>(smem) + wave * 64 * D;
   Wave<DT, D> w;
-  check_offsets(p);
+  check_sequences(p);
   const bool prefix = (int)blockIdx.x < p.prefix_blocks;
   PrefixItem x;
   int part;
@@ -969,7 +970,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attend_wide(PrefixDev p) {
   __shared__ OwnRow s_own[NW][32];
   __shared__ int s_page[NW][32];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  check_offsets(p);
+  check_sequences(p);
   const bool prefix = (int)blockIdx.x < p.prefix_blocks;
   PrefixItem x;
   int part;

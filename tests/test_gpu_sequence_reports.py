@@ -126,3 +126,22 @@ def test_attention_reports_offsets_of_many_groups():
     for go, code in ((good, 0), (beyond, E.EMB_E_INVAL), (last, E.EMB_E_INVAL)):
         run_attention(cache, q, 0.125, None, i32(lens), table, (i32(go), i32([40] * 400), pages))
         assert reported(cache) == code
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+def test_attention_reports_prefixes_that_their_tables_do_not_hold(kernel):
+    hq, hk = KERNELS[kernel]
+    off = [0, 3, 5, 8]
+    table_of = lambda n: torch.zeros((1, n), dtype=torch.int32, device="cuda")
+    run = lambda n, width, go=(0, 3): attention(hq, hk, off, groups=lambda good: (
+        i32(go), i32(n), table_of(width).repeat(len(n), 1)))
+    assert run([32], 2) == 0 and run([0], 0) == 0 and run([0], 2) == 0
+    assert run([33], 2) == E.EMB_E_BOUNDS
+    assert run([-1], 2) == E.EMB_E_BOUNDS
+    assert run([5], 0) == E.EMB_E_BOUNDS          # no page at all: nothing but the lengths tells
+    assert run([-1], 0) == E.EMB_E_BOUNDS
+    assert run([0, 9], 0, (0, 3, 3)) == E.EMB_E_BOUNDS
+    # the same of a group without sequences, among few and among many
+    assert run([16, 99], 2, (0, 3, 3)) == E.EMB_E_BOUNDS
+    assert run([16] + [0] * 300, 2, [0] + [3] * 301) == 0
+    assert run([16] + [0] * 299 + [99], 2, [0] + [3] * 301) == E.EMB_E_BOUNDS
