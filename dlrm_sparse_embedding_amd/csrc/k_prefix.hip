@@ -525,7 +525,9 @@ __device__ __forceinline__ OwnTile own_look(const PrefixDev& p, const OwnRow& r,
 // an infinity or NaN that its row does not see (0 * infinity), so tiles with such
 // values are left out (the return value tells) and taken by a second call with
 // WINDOWS: one product for each limit among the sequence's rows with the values
-// beyond it cleared, of which each row keeps its own.
+// beyond it cleared, of which each row keeps its own. The products add to the outputs
+// as the first call's do, and a tile with values that a row does not see is that row's
+// last one: every bit is what it is without them.
 template <int DT, int D, bool WINDOWS>
 __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, const OwnRow& r, OwnTile next, int h,
                                           int step, short* v) {
@@ -596,11 +598,11 @@ __device__ __forceinline__ bool own_tiles(const PrefixDev& p, Wave<DT, D>& w, co
       const bool takes = mine && r.seen == lim;
 #pragma unroll
       for (int d = 0; d < D / 32; ++d) {
-        f16v o = {};
+        f16v o = w.o[d];
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) o = mfma<DT>(operand_v<D>(vt, kk, d), prob[kk], o);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) w.o[d][c] += takes ? o[c] : 0.f;
+        for (int c = 0; c < 16; ++c) w.o[d][c] = takes ? o[c] : w.o[d][c];
       }
     }
   }
