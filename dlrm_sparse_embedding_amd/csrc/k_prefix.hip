@@ -90,6 +90,7 @@ __device__ __forceinline__ float both_halves_sum(float x) {
 struct PrefixDev {
   PrefixArgs a;
   float scale2;  // |scale| * log2(e), never 0
+  bool zero;     // the scale is 0
   uint32_t q_sign;  // sign bits of two elements where the scale is negative
   int m;         // query heads of a cache head
   FastDiv by_m;
@@ -157,6 +158,16 @@ struct Wave {
   float sum;  // this lane's part of the sum
 };
 
+// 0 for each finite element, NaN for the others.
+template <int DT>
+__device__ __forceinline__ u4 times_zero(u4 x) {
+  constexpr uint32_t top = DT == EMB_BF16 ? 0x7f80u : 0x7c00u;
+  auto one = [](uint32_t w) {
+    return ((w & top) == top ? 0x7fffu : 0u) | ((w >> 16 & top) == top ? 0x7fff0000u : 0u);
+  };
+  return u4{one(x.x), one(x.y), one(x.z), one(x.w)};
+}
+
 template <int DT, int D>
 __device__ __forceinline__ void load_q(const PrefixDev& p, const Rows& it, Wave<DT, D>& w) {
   const int lane = threadIdx.x & 63;
@@ -169,6 +180,7 @@ __device__ __forceinline__ void load_q(const PrefixDev& p, const Rows& it, Wave<
   for (int s = 0; s < D / 16; ++s) {
     u4 x = *reinterpret_cast<const u4*>(src + 16 * s + 8 * (lane >> 5));
     x ^= p.q_sign;  // a negative scale is taken into q, so that maxima stay maxima
+    if (p.zero) x = times_zero<DT>(x);
     w.q[s] = __builtin_bit_cast(s8v, x);
   }
 #pragma unroll
@@ -1143,9 +1155,11 @@ hipError_t launch(const PrefixDev& p, int blocks, bool wide, hipStream_t st) {
 hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& plan, char* ws, hipStream_t st) {
   PrefixDev p{};
   p.a = a;
-  // a scale of 0 would turn a masked -infinity into NaN; 1e-37 scales every
-  // finite product of 16-bit operands to less than half a step of 1
-  p.scale2 = std::max(std::fabs(a.scale) * 1.4426950408889634f, 1e-37f);
+  // A scale of 0 would turn a masked -infinity into NaN: the queries become 0
+  // instead. The smallest others are subnormal here, at most 2^-150 off, which
+  // moves a score (of products below 2^128) by at most 2^-22.
+  p.zero = a.scale == 0.f;
+  p.scale2 = p.zero ? 1.f : std::fabs(a.scale) * 1.4426950408889634f;
   p.q_sign = a.scale < 0.f ? 0x80008000u : 0u;
   p.m = a.q_heads / a.kv.heads;
   p.by_m = fast_div((uint32_t)p.m);
