@@ -439,7 +439,8 @@ int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim,
   if (rc) return rc;
   if ((rc = check_cache(kv, dtype, kv->v.heads, dim))) return rc;
   if ((rc = check_seqs(offsets, tokens, seqs, lens, table, table_width))) return rc;
-  if (!std::isfinite(scale)) return fail(EMB_E_INVAL, "scale is not finite");
+  // the kernels hold scale * log2(e) in fp32
+  if (!(std::fabs(scale) <= 0x1p127f)) return fail(EMB_E_INVAL, "scale is not a number within +- 2^127");
   if (groups > 0) {
     if (!group_offsets || !prefix_lens || !aligned(group_offsets, 4) || !aligned(prefix_lens, 4))
       return fail(EMB_E_INVAL, "group_offsets/prefix_lens is NULL or misaligned");

@@ -627,6 +627,7 @@ int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dty
  * groups = 0: no prefixes (the three pointers NULL).
  *     out = sum_j softmax_j(scale * q . k_j) v_j,
  *     lse = ln sum_j exp(scale * q . k_j)      (fp32 [tokens][q_heads], or NULL)
+ * scale: any number within +- 2^127 (EMB_E_INVAL otherwise).
  * A query that sees no slot gets zeros and -inf. Slots that a query does not
  * see have no influence on it, whatever they hold, nor has what other
  * sequences of the call hold; reruns are bit-identical.
