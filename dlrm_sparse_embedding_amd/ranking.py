@@ -40,7 +40,6 @@ class HistoryRanker:
         self.cache = E.KVCache(torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2),
                                torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2))
         self.next_page = 0
-        self.ws = torch.empty(0, dtype=torch.uint8, device="cuda")
 
     def close(self) -> None:
         self.tables.close()
@@ -106,12 +105,12 @@ class HistoryRanker:
                         eps=self.eps if self.norm else None, positions=place)
         need = E.emb_prefix_attention_workspace_bytes(self.cache.handle, n, self.heads, history_lens.numel(),
                                                       history_table.shape[1], table.shape[1])
-        if self.ws.numel() < need:
-            self.ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        # a call's own: calls on other streams may be under way
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
         out = torch.empty_like(qr)
         lse = torch.empty((n, self.heads), device="cuda")
         E.emb_prefix_attention(self.cache.handle, qr, out, 1 / math.sqrt(self.dim), None, one, table, group_offsets,
-                               history_lens, history_table, self.ws, lse=lse)
+                               history_lens, history_table, ws, lse=lse)
         return out, lse
 
     # ---- training ----
