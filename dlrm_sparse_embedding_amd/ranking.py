@@ -31,7 +31,10 @@ class HistoryRanker:
         self.tables.init_uniform(seed)
         gen = torch.Generator(device="cuda").manual_seed(seed)
         out = (heads + 2 * kv_heads) * dim
-        self.proj = torch.randn((width, out), generator=gen, device="cuda").mul_(4 / math.sqrt(width)).to(dtype)
+        # Steps are taken on fp32 weights, most of them being less than half a step of a 16-bit one; proj is their
+        # rounded copy, written after each. Weights from elsewhere go into both.
+        self.master = torch.randn((width, out), generator=gen, device="cuda").mul_(4 / math.sqrt(width))
+        self.proj = self.master.to(dtype)
         self.wq = torch.ones(dim, device="cuda") if norm else None
         self.wk = torch.ones(dim, device="cuda") if norm else None
         self.norm = norm
@@ -136,7 +139,9 @@ class HistoryRanker:
         gq, gk, dwq, dwk = self.place_backward(q, k, positions, dq, dk)
         g = torch.cat([gq, gk, dv], 1).view(ids.numel(), -1)
         d_rows = (g @ self.proj.t()).float()
-        self.proj -= (lr * (rows.to(self.dtype).t() @ g).float()).to(self.dtype)
+        # both products sum in fp32 and round once to the type of the heads
+        self.master -= lr * (rows.to(self.dtype).t() @ g).float()
+        self.proj.copy_(self.master)
         if self.norm:
             self.wq -= lr * dwq
             self.wk -= lr * dwk
