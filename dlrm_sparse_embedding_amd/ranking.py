@@ -42,7 +42,8 @@ class HistoryRanker:
         shape = (pages, kv_heads, page, dim)       # a page holds each head's rows together
         self.cache = E.KVCache(torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2),
                                torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2))
-        self.next_page = 0
+        self.next_page = 0        # pages from here on were never handed out
+        self.returned = []        # pages handed back
 
     def close(self) -> None:
         self.tables.close()
@@ -80,13 +81,25 @@ class HistoryRanker:
     def new_pages(self, counts) -> torch.Tensor:
         """A page table row for each of `counts` slots; -1 behind the last page."""
         need = [-(-int(c) // self.page) for c in counts]
-        if self.next_page + sum(need) > self.cache.pages:
+        if sum(need) > len(self.returned) + self.cache.pages - self.next_page:
             raise ValueError("the cache has no pages left")
         table = torch.full((len(need), max(need + [1])), -1, dtype=torch.int32)
         for row, n in zip(table, need):
-            row[:n] = torch.arange(self.next_page, self.next_page + n, dtype=torch.int32)
-            self.next_page += n
+            again = min(n, len(self.returned))
+            if again:
+                row[:again] = torch.tensor(self.returned[-again:], dtype=torch.int32)
+                del self.returned[-again:]
+            row[again:n] = torch.arange(self.next_page, self.next_page + n - again, dtype=torch.int32)
+            self.next_page += n - again
         return table.cuda()
+
+    def return_pages(self, table) -> None:
+        """Hands back the pages of new_pages' table rows, for later rows. Work on them has to be done, or under way
+        on the stream that will use them next."""
+        pages = [p for p in table.flatten().tolist() if p >= 0]
+        if len(set(pages)) != len(pages) or any(p >= self.next_page for p in pages) or set(pages) & set(self.returned):
+            raise ValueError("a page that is not handed out")
+        self.returned += pages
 
     def append(self, ids, offsets, lens, table, positions=None) -> None:
         """Writes the items' keys and values to their sequences' pages (offsets, lens, table: emb_kv_append)."""
@@ -177,8 +190,8 @@ def main() -> None:
     table = r.new_pages([a.history] * a.users)
     ids = torch.randint(0, items, (a.candidates,), generator=gen, device="cuda")
     groups = torch.linspace(0, a.candidates, a.users + 1, device="cuda").to(torch.int32)
-    own = r.new_pages([1] * a.candidates)
     for _ in range(2):      # the first calls load kernels
+        own = r.new_pages([1] * a.candidates)
         timed(f"append {history.numel()} items", lambda: r.append(history, offsets, lens, table))
         out, _ = timed(f"rank {a.candidates} candidates of {a.users} users",
                        lambda: r.rank(ids, groups, lens, table, own))
@@ -186,6 +199,7 @@ def main() -> None:
                  for n in (r.heads, r.kv_heads, r.kv_heads)]
         places = torch.full((ids.numel(),), a.history, dtype=torch.int64, device="cuda")
         timed("training step", lambda: r.train_step(ids, places, *grads, lr=0.01))
+        r.return_pages(own)
     r.cache.check_error()
     r.tables.check_device_error()
     print(f"mean |output| {out.float().abs().mean().item():.4f}")
