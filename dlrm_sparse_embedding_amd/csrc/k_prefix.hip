@@ -364,17 +364,16 @@ __device__ __forceinline__ int swizzle_v(int r) {
 typedef __attribute__((address_space(3))) short lds_short;
 
 // 16 bytes for each active lane from base + off into LDS at `at` + 16 * lane.
-// The compiler does not see the transfer: the caller waits (wait_fetch) and
-// passes a barrier before anyone reads. It does not see the instruction's
-// hazards either: a base that a vector instruction wrote would have to be five
-// wait states old, so a scalar one copies it, and that copy is the wait state
-// which m0 needs. (m0 has no other user here: LDS accesses need none on this
-// architecture, and no register is indexed.)
+// `at` is an operand in m0, so the compiler knows what the register holds. It
+// does not see the transfer: the caller waits (wait_fetch) and passes a barrier
+// before anyone reads. It does not see the instruction's hazards either: a base
+// that a vector instruction wrote would have to be five wait states old, so a
+// scalar one copies it, and that copy is the wait state which m0 needs.
 __device__ __forceinline__ void fetch16(uint64_t base, uint32_t off, uint32_t at) {
   uint64_t from;
-  asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
+  asm volatile("s_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
                : "=&s"(from)
-               : "s"(at), "v"(off), "s"(base)
+               : "{m0}"(at), "v"(off), "s"(base)
                : "memory");
 }
 __device__ __forceinline__ void wait_fetch() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
@@ -383,9 +382,9 @@ __device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0
 
 // The same with an address for each lane.
 __device__ __forceinline__ void fetch16(uint64_t from, uint32_t at) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(at), "v"(from)
+               : "{m0}"(at), "v"(from)
                : "memory");
 }
 
