@@ -180,8 +180,11 @@ __device__ __forceinline__ void load_q(const PrefixDev& p, const Rows& it, Wave<
   for (int s = 0; s < D / 16; ++s) {
     u4 x = *reinterpret_cast<const u4*>(src + 16 * s + 8 * (lane >> 5));
     x ^= p.q_sign;  // a negative scale is taken into q, so that maxima stay maxima
-    if (p.zero) x = times_zero<DT>(x);
     w.q[s] = __builtin_bit_cast(s8v, x);
+  }
+  if (p.zero) {  // once, behind all of the loads
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) w.q[s] = __builtin_bit_cast(s8v, times_zero<DT>(__builtin_bit_cast(u4, w.q[s])));
   }
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) w.o[d] = f16v{};
@@ -755,11 +758,14 @@ __device__ __forceinline__ bool own_item(const PrefixDev& p, int block, Rows* it
 // not hold, spread over the grid.
 __device__ __forceinline__ void check_sequences(const PrefixDev& p) {
   if (p.a.offsets) report_offsets(p.a.offsets, p.a.seqs, p.a.tokens, p.a.kv.error);
-  if (p.a.groups == 0) return;
-  report_offsets(p.a.group_offsets, p.a.groups, p.a.seqs, p.a.kv.error);
+  if (!p.a.kv.error) return;
   const long long cap = (long long)p.a.pwidth * p.a.kv.page;
-  for (long long g = (long long)blockIdx.x * 256 + threadIdx.x; g < p.a.groups; g += (long long)gridDim.x * 256)
-    if (p.a.prefix_lens[g] < 0 || p.a.prefix_lens[g] > cap) flag(p, kKvBadPage);
+  for (long long g = (long long)blockIdx.x * 256 + threadIdx.x; g < p.a.groups; g += (long long)gridDim.x * 256) {
+    const int a = p.a.group_offsets[g], b = p.a.group_offsets[g + 1], len = p.a.prefix_lens[g];
+    const int bits = (breaks_offsets(a, b, g, p.a.groups, p.a.seqs) ? kKvBadOffsets : 0) |
+                     (len < 0 || len > cap ? kKvBadPage : 0);
+    if (bits) flag(p, bits);
+  }
 }
 
 // Few rows: a block takes one tile of 32 rows, a cache head and a part of the
