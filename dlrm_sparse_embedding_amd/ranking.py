@@ -61,7 +61,7 @@ class HistoryRanker:
 
     def project(self, rows: torch.Tensor) -> torch.Tensor:
         """[n, heads + 2 kv_heads, dim]: queries, keys, values."""
-        return (rows.to(self.dtype) @ self.proj).view(rows.shape[0], -1, self.dim)
+        return (rows.to(self.dtype) @ self.proj).view(rows.shape[0], self.heads + 2 * self.kv_heads, self.dim)
 
     def parts(self, fused):
         h, k = self.heads, self.kv_heads
@@ -150,7 +150,7 @@ class HistoryRanker:
         rows = self.rows(ids)
         q, k, _ = self.parts(self.project(rows))
         gq, gk, dwq, dwk = self.place_backward(q, k, positions, dq, dk)
-        g = torch.cat([gq, gk, dv], 1).view(ids.numel(), -1)
+        g = torch.cat([gq, gk, dv], 1).view(ids.numel(), self.proj.shape[1])
         d_rows = (g @ self.proj.t()).float()
         # both products sum in fp32 and round once to the type of the heads
         self.master -= lr * (rows.to(self.dtype).t() @ g).float()

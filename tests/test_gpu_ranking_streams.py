@@ -55,3 +55,24 @@ def test_streams_rank_at_once():
             assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     r.cache.check_error()
     r.close()
+
+
+def test_calls_without_items():
+    # a step in which nobody has anything: no history item, no candidate, no training example
+    r, asked = ranker([30], [600, 50])
+    want = [t.clone() for t in r.rank(*asked[0])]
+    none = torch.empty(0, dtype=torch.int64, device="cuda")
+    kept = r.cache.k.clone(), r.cache.v.clone(), r.proj.clone(), r.tables.weights[0][0].clone()
+    r.append(none, i32([0, 0]), i32([0]), r.new_pages([0]))
+    r.append(none, i32([0]), i32([]), r.new_pages([]))
+    out, lse = r.rank(none, i32([0, 0]), i32([600]), asked[0][3][:1].contiguous(), r.new_pages([]))
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4)
+    grads = [torch.empty((0, n, 64), dtype=torch.bfloat16, device="cuda") for n in (4, 2, 2)]
+    r.train_step(none, none, *grads, lr=0.1)
+    r.cache.check_error()
+    r.tables.check_device_error()
+    for a, b in zip(kept, (r.cache.k, r.cache.v, r.proj, r.tables.weights[0][0])):
+        assert torch.equal(a, b)
+    for a, b in zip(want, r.rank(*asked[0])):
+        assert torch.equal(a, b)
+    r.close()
