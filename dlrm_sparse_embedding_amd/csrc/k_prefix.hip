@@ -33,8 +33,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "emb_device.h"
-#include "seq_internal.h"
+#include "seq_device.h"
 
 namespace emb {
 

@@ -26,8 +26,7 @@
 // the launch: 3 to 5 us on the device, 7 to 9 through the binding.
 #include <algorithm>
 
-#include "emb_device.h"
-#include "seq_internal.h"
+#include "seq_device.h"
 
 namespace emb {
 
