@@ -24,12 +24,15 @@
 // the unrounded ones). They are scaled by 2^8, so that fp16 keeps its full
 // precision down to 2^-22 of a row's largest.
 //
-// Measured: 1024 queries over 32768 slots (32 x 8 heads of 128) 572 us, 963
+// Measured: 1024 queries over 32768 slots (32 x 8 heads of 128) 555 us, 990
 // TFLOP/s, where a large library product reaches 1391; the matrix units are
-// busy half of the cycles, at 1.8 GHz. 24 groups' 2400 queries over prefixes of
-// 512 to 2048 and 20 own slots 104 us (2.4 TB/s), 509 queries over 8191 slots
-// (16 heads of 64) 46 us, 8 over 4096 slots 21 us: the last two are chains of
-// dependent reads (offsets, lengths, pages, keys) and two launches.
+// busy half of the cycles, at 1.85 GHz. 24 groups' 2400 queries over prefixes of
+// 512 to 2048 and 20 own slots 101 us (2.5 TB/s), 509 queries over 8191 slots
+// (16 heads of 64) 44 us, 8 over 4096 slots 21 us: the last two are chains of
+// dependent reads (offsets, lengths, pages, keys) and two launches. Own
+// sequences alone: 64 queries over 2000 slots each 111 us (4.7 TB/s), a prompt
+// of 2000 queries 170 us (195 TFLOP/s: each wave reads its sequence's slots for
+// itself).
 #include <algorithm>
 #include <cmath>
 

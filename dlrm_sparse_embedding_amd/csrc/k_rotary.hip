@@ -7,8 +7,8 @@
 //   gradient  u = R^T dy,  n = x r,  dx = r (u w - n mean(u w n)),  dw = sum u n
 // All of it is one pass over the heads: bound by memory. Angles are integers:
 // pair i's frequency is a 64-bit fraction of a turn, so position * frequency
-// modulo 2^64 is exact however far the position is; sine and cosine come from
-// the Taylor series on an eighth of a turn to either side of a quadrant's
+// modulo 2^64 loses nothing but the frequency's rounding times the position
+// (2^-31 of a turn at 2^32); sine and cosine come from the Taylor series on an eighth of a turn to either side of a quadrant's
 // middle (terms to x^9 and x^10, truncation below 5e-9).
 //
 // Layout. A lane owns one "unit": 2 V elements (V = 16 bytes' worth) that hold
@@ -20,7 +20,7 @@
 //
 // Measured (a large copy reaches 5.4 TB/s read and written): rotation of 16384 x
 // 32 x 64 fp32 58 us (4.6 TB/s), norm of 16384 x 40 x 128 bf16 62 us (5.4), its
-// gradient for 12289 tokens 98 us (3.8; the vector units are 40% busy, neither
+// gradient for 12289 tokens 97 us (3.9; the vector units are 43% busy, neither
 // more loads in flight nor more blocks change it), append of 20011 x 8 x 128
 // bf16 with norm 39 us (4.2; rows scattered over pages). Small calls are bound by
 // the launch: 3 to 5 us on the device, 7 to 9 through the binding.
@@ -91,7 +91,8 @@ __device__ __forceinline__ u4 narrow(const float* in) {
 
 // Sine and cosine of pos * turn / 2^64 turns. The phase's upper 32 bits are
 // kept (2^-32 of a turn); what is left after the nearest quarter is at most an
-// eighth of a turn.
+// eighth of a turn, up to 2^29 units, which fp32 rounds by up to 16: 2^-28 of a
+// turn, less than half a step of fp32 at 1.
 __device__ __forceinline__ void sincos_turn(uint64_t turn, long long pos, float mag, float* c, float* s) {
   const uint32_t ph = (uint32_t)((turn * (uint64_t)pos) >> 32);
   const uint32_t quad = (ph + 0x20000000u) >> 30;
@@ -339,9 +340,9 @@ struct Unit {
 };
 
 // 16 bytes at element i. Every element is read once, so reads pass the L2 by;
-// writes do (PAST) where a store instruction fills whole lines: an append of
-// 20011 tokens 46 -> 42 us, norm of 16384 x 40 heads 76 -> 66, its gradient 105
-// -> 99. Parts of lines that pass the L2 by are written several times (rotation
+// writes do (PAST) where a store instruction fills whole lines. Together with
+// neighbouring heads in a wave's accesses: an append of 20011 tokens 48 -> 42 us,
+// norm of 16384 x 40 heads 76 -> 68, its gradient 105 -> 99. Parts of lines that pass the L2 by are written several times (rotation
 // of half of each 192-byte head 27 -> 45 us).
 template <int DT>
 __device__ __forceinline__ u4 get16(const void* p, long long i) {

@@ -17,7 +17,7 @@ int hip_fail(hipError_t e, const char* what);
 
 // Frequencies of a rotation. turn[i] is pair i's angle per position as a
 // fraction of a whole turn, in units of 2^-64: position * turn[i] modulo 2^64
-// is the angle, whole turns dropped, without any rounding.
+// is the angle, whole turns dropped, with no rounding but the frequency's own.
 struct RotTable {
   uint64_t turn[EMB_MAX_ROT / 2];
   float mag;

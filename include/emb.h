@@ -488,9 +488,10 @@ int emb_probe_update(const float* src, int64_t nsrc, float* a, float* b, int64_t
  *                   are stretched
  *   EMB_ROT_BANDS   the same with keep = (turns - turns_low) / (turns_high -
  *                   turns_low)
- * Angles are exact to 2^-31 of a turn for positions below 2^20 in magnitude
- * (the frequency is held as a 64-bit fraction of a turn and multiplied by the
- * position in integers; the error grows with the position from there). */
+ * Angles are within 2^-27 of a turn (5e-8 radians) for positions below 2^32 in
+ * magnitude: the phase is rounded to fp32 (up to 2^-28), and the frequency is
+ * held as a 64-bit fraction of a turn and multiplied by the position in
+ * integers, so that its own rounding grows with the position. */
 #define EMB_ROT_HALF         0
 #define EMB_ROT_INTERLEAVED  1
 
@@ -568,7 +569,8 @@ int emb_qk_norm_rotary_backward(const emb_rotary* rot, const void* positions, in
  * k and v hold `pages` pages of `page` slots of `heads` heads of `dim`
  * elements; element (p, s, h, c) of k lies at k[p * k_page_stride + s *
  * k_slot_stride + h * k_head_stride + c], v likewise. A sequence's page table
- * row lists the pages of its slots 0.., page by page. */
+ * row lists the pages of its slots 0.., page by page. In a cache that is
+ * appended to no two (page, slot, head) share elements. */
 typedef struct emb_kv_desc {
   void*   k;
   void*   v;
@@ -637,6 +639,13 @@ int emb_kv_append(emb_kv* kv, const emb_rotary* rot, int64_t tokens, int32_t dty
  * probabilities are rounded to the cache's type for the matrix product.
  * Offsets and group offsets that break their contract anywhere raise the
  * cache's error flag; the call's results are then unspecified.
+ * Speed: the host knows the tables' widths, not the lengths, and splits the
+ * slots by them, so tables should not be much wider than the lengths need. Up to
+ * 256 slots of table_width own slots go along with the prefix; beyond them they
+ * are taken on their own, with partial outputs and a second launch (1200 queries
+ * over 24 prefixes of 1024 and 40 own slots: 122 us with a table of 64 slots,
+ * 128 with one of 2048). Many queries share a prefix' slots in LDS
+ * where a page is a multiple of 8 slots, otherwise only 32 rows do.
  * ws: device, 16-byte aligned, at least
  * emb_prefix_attention_workspace_bytes (0 on invalid arguments). */
 size_t emb_prefix_attention_workspace_bytes(const emb_kv* kv, int64_t tokens, int32_t q_heads, int32_t groups,
