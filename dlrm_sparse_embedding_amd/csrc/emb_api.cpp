@@ -209,7 +209,6 @@ int check_pool(int pool) {
   return EMB_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
 

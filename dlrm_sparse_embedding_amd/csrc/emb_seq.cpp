@@ -17,22 +17,10 @@ struct emb_rotary {
   RotTable t;
 };
 
-struct emb_kv {
-  KvView v;
-};
-
-namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-int esize(int dtype) { return dtype == EMB_F32 ? 4 : 2; }
+namespace emb {
 
 int check_dtype(int dtype) {
   if (dtype != EMB_F32 && dtype != EMB_BF16 && dtype != EMB_F16) return fail(EMB_E_DTYPE, "unknown dtype %d", dtype);
-  return EMB_OK;
-}
-
-int check_itype(int itype) {
-  if (itype != EMB_I32 && itype != EMB_I64) return fail(EMB_E_DTYPE, "itype %d is not EMB_I32/EMB_I64", itype);
   return EMB_OK;
 }
 
@@ -57,6 +45,21 @@ int check_out(const char* name, const Heads& h, long long tokens, int dim, int d
   return EMB_OK;
 }
 
+int check_norm(const char* name, const float* w, float eps) {
+  if (w && !aligned(w, 16)) return fail(EMB_E_INVAL, "%s is not 16-byte aligned", name);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(EMB_E_INVAL, "eps must be finite and >= 0");
+  return EMB_OK;
+}
+
+}  // namespace emb
+
+namespace {
+
+int check_itype(int itype) {
+  if (itype != EMB_I32 && itype != EMB_I64) return fail(EMB_E_DTYPE, "itype %d is not EMB_I32/EMB_I64", itype);
+  return EMB_OK;
+}
+
 // Overlap of two operands is only allowed as the very same view.
 int check_in_place(const char* in_name, const Heads& in, const char* out_name, const Heads& out) {
   if (in.p == out.p && (in.ts != out.ts || in.hs != out.hs))
@@ -78,12 +81,6 @@ int check_common(const emb_rotary* rot, const void* positions, int itype, int64_
     if (!positions) return fail(EMB_E_INVAL, "positions is NULL");
     if (!aligned(positions, itype == EMB_I64 ? 8 : 4)) return fail(EMB_E_INVAL, "positions are misaligned");
   }
-  return EMB_OK;
-}
-
-int check_norm(const char* name, const float* w, float eps) {
-  if (w && !aligned(w, 16)) return fail(EMB_E_INVAL, "%s is not 16-byte aligned", name);
-  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(EMB_E_INVAL, "eps must be finite and >= 0");
   return EMB_OK;
 }
 

@@ -45,10 +45,7 @@ namespace {
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef short s8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
 typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
-typedef _Float16 hf2 __attribute__((ext_vector_type(2)));
-typedef float fl2 __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) s4v lds_s4v;
 
@@ -102,10 +99,6 @@ struct PrefixDev {
   float* part_o;
   float* part_lse;
 };
-
-__device__ __forceinline__ int div_by(const FastDiv d, int n) {
-  return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift);
-}
 
 __device__ __forceinline__ void flag(const PrefixDev& p, int bit) {
   if (p.a.kv.error) atomicOr(p.a.kv.error, bit);

@@ -15,6 +15,9 @@ int fail(int code, const char* fmt, ...);
 int ok();
 int hip_fail(hipError_t e, const char* what);
 
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+inline int esize(int dtype) { return dtype == EMB_F32 ? 4 : 2; }
+
 // Frequencies of a rotation. turn[i] is pair i's angle per position as a
 // fraction of a whole turn, in units of 2^-64: position * turn[i] modulo 2^64
 // is the angle, whole turns dropped, with no rounding but the frequency's own.
@@ -31,6 +34,12 @@ struct Heads {
   long long ts, hs;
   int n;
 };
+
+// Checks of arguments (emb_seq.cpp); EMB_OK or the code of a reported failure.
+int check_dtype(int dtype);
+int check_heads(const char* name, const Heads& h, int dtype);
+int check_out(const char* name, const Heads& h, long long tokens, int dim, int dtype);
+int check_norm(const char* name, const float* w, float eps);
 
 // n / d for 0 <= n < 2^31 as a product and a shift: with s = ceil(log2 d) and
 // mul = floor(2^(31+s) / d) + 1, n * mul >> (31 + s) is exact.
@@ -134,4 +143,48 @@ PrefixPlan prefix_plan(const KvView& kv, long long tokens, int q_heads, int grou
                        int width);
 hipError_t launch_prefix_attention(const PrefixArgs& a, const PrefixPlan& p, char* ws, hipStream_t st);
 
+// ---- layer norm and dropout (k_rows.hip) ----
+// [rows][dim] in memory; stride in elements.
+struct Rows2D {
+  const void* p;
+  long long stride;
+  int dtype;
+};
+
+struct LayerNormArgs {
+  long long rows;
+  int dim;
+  Rows2D x, y;  // y.p is written
+  const float *w, *b;
+  float eps;
+};
+hipError_t launch_layer_norm(const LayerNormArgs& a, hipStream_t st);
+
+struct LayerNormBackArgs {
+  long long rows;
+  int dim;
+  Rows2D x, dy, dx;
+  const float* w;
+  float eps;
+  float* part;  // [blocks][2][dim]
+  float *dw, *db;
+};
+int layer_norm_back_blocks(long long rows, int dim);  // upper bound
+hipError_t launch_layer_norm_back(const LayerNormBackArgs& a, hipStream_t st);
+
+struct DropoutArgs {
+  long long rows;
+  int dim;
+  Rows2D x, res, y;  // res.p may be null
+  uint64_t threshold;  // t of p = t / 2^32, at most 2^32
+  float scale;         // 1 / (1 - p)
+  uint64_t seed;
+  const long long* step;  // may be null
+};
+hipError_t launch_dropout(const DropoutArgs& a, hipStream_t st);
+
 }  // namespace emb
+
+struct emb_kv {
+  emb::KvView v;
+};

@@ -193,6 +193,15 @@ def lib() -> ctypes.CDLL:
     L.emb_prefix_attention.argtypes = [vp, i64, i32, i32] + heads_io * 2 + [i32, f32, vp, i32, vp, vp, i32, vp, i32, vp, vp, i32,
                                                                   vp, sz, vp, vp]
     L.emb_prefix_attention.restype = ctypes.c_int
+    rows_io = [vp, i32, i64]
+    L.emb_layer_norm.argtypes = [i64, i32] + rows_io * 2 + [vp, vp, f32, vp]
+    L.emb_layer_norm.restype = ctypes.c_int
+    L.emb_layer_norm_workspace_bytes.argtypes = [i64, i32]
+    L.emb_layer_norm_workspace_bytes.restype = sz
+    L.emb_layer_norm_backward.argtypes = [i64, i32] + rows_io * 2 + [vp, i64, vp, f32, vp, sz, vp, vp, vp]
+    L.emb_layer_norm_backward.restype = ctypes.c_int
+    L.emb_dropout.argtypes = [i64, i32, i32] + [vp, i64] * 3 + [ctypes.c_double, ctypes.c_uint64, vp, vp]
+    L.emb_dropout.restype = ctypes.c_int
     _lib = L
     return L
 
@@ -598,6 +607,65 @@ def emb_prefix_attention(kv: int, q, out, scale: float, offsets, lens, table, gr
         kv, T, _dtype_code("q", q), D, *_heads("q", q, T, D, q.dtype), *_heads("out", out, T, D, q.dtype), hq, float(scale),
         *_sequences(T, offsets, lens, table), *groups, ws_p, ws_n,
         None if lse is None else _dense("lse", lse, torch.float32, (T, hq)), _stream_for(q, stream)))
+
+
+# ---- history layer ---------------------------------------------------------------
+
+def _rows(name: str, t: torch.Tensor, shape, dtype=None):
+    """Checks a [rows, dim] operand; its (pointer, row stride)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if dtype is not None and t.dtype is not dtype:
+        raise ValueError(f"{name} is {t.dtype}, not {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} is not in device memory")
+    stride, es = t.stride()
+    if es != 1 and shape[1] > 1:
+        raise ValueError(f"the elements of one row of {name} must be contiguous")
+    return t.data_ptr(), stride
+
+
+def _rows_shape(x: torch.Tensor):
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, dim]")
+    return x.shape
+
+
+def emb_layer_norm(x, y, w, b, eps: float, stream=None) -> None:
+    """x, y: [rows, dim], any row stride; y is of x's type, or bf16 or fp16 for an fp32 x, and may be x. w, b: fp32
+    [dim] or None."""
+    R, D = _rows_shape(x)
+    xp, xs = _rows("x", x, x.shape)
+    yp, ys = _rows("y", y, x.shape)
+    _check(lib().emb_layer_norm(R, D, xp, _dtype_code("x", x), xs, yp, _dtype_code("y", y), ys, _weight("w", w, D),
+                                _weight("b", b, D), float(eps), _stream_for(x, stream)))
+
+
+def emb_layer_norm_workspace_bytes(rows: int, dim: int) -> int:
+    return int(lib().emb_layer_norm_workspace_bytes(int(rows), int(dim)))
+
+
+def emb_layer_norm_backward(x, dy, dx, w, eps: float, ws, dw=None, db=None, stream=None) -> None:
+    """Gradients of emb_layer_norm: dx (of x's type; may be x or dy) and, where given, dw and db (fp32 [dim])."""
+    R, D = _rows_shape(x)
+    xp, xs = _rows("x", x, x.shape)
+    yp, ys = _rows("dy", dy, x.shape)
+    ws_p, ws_n = _workspace(ws)
+    _check(lib().emb_layer_norm_backward(R, D, xp, _dtype_code("x", x), xs, yp, _dtype_code("dy", dy), ys,
+                                         *_rows("dx", dx, x.shape, x.dtype), _weight("w", w, D), float(eps), ws_p,
+                                         ws_n, _weight("dw", dw, D), _weight("db", db, D), _stream_for(x, stream)))
+
+
+def emb_dropout(x, y, p: float, seed: int, step=None, residual=None, stream=None) -> None:
+    """y = dropout(x) [+ residual], [rows, dim] of one type, any row strides; y may be x or residual. The mask is a
+    function of row, column, seed (64 bits) and step (int64 [1] in device memory, or None for 0)."""
+    R, D = _rows_shape(x)
+    xp, xs = _rows("x", x, x.shape)
+    rp, rs = (None, 0) if residual is None else _rows("residual", residual, x.shape, x.dtype)
+    _check(lib().emb_dropout(R, D, _dtype_code("x", x), xp, xs, rp, rs, *_rows("y", y, x.shape, x.dtype), float(p),
+                             int(seed) & 0xFFFFFFFFFFFFFFFF,
+                             None if step is None else _dense("step", step, torch.int64, (1,)),
+                             _stream_for(x, stream)))
 
 
 class Rotary:

@@ -657,6 +657,67 @@ int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim,
                          const int32_t* prefix_lens, const int32_t* prefix_table, int32_t prefix_width, void* ws,
                          size_t ws_bytes, float* lse, void* hip_stream);
 
+/* ======================================================================
+ * History layer: what trains a layer over users' histories, next to the
+ * operators above. Layer norm with its gradient, and dropout. The conventions
+ * are those of the sequence operators.
+ *
+ * A "rows" operand is [rows][dim] in device memory, given as a pointer and a
+ * row stride in elements; the dim elements of a row are contiguous. Operands
+ * that are written must not have overlapping rows, and must not overlap
+ * another operand unless the call allows that it is the same one.
+ * ====================================================================== */
+
+#define EMB_MAX_ROW_DIM 16384   /* largest dim of emb_layer_norm */
+
+/* ---- layer norm ----------------------------------------------------------
+ *     y = (x - m) r w + b,  m = mean of the row, r = 1 / sqrt(mean (x - m)^2 + eps)
+ * for each row; w and b are fp32 [dim], 16-byte aligned (NULL: ones, zeros).
+ * x_dtype is x's type, y_dtype that of y: the same, or EMB_BF16 / EMB_F16 for
+ * an EMB_F32 x (rows of a table on their way to a 16-bit product). Rows are
+ * read once; mean and variance are fp32, the variance of the differences from
+ * the mean. y may be x with the same type and stride. 1 <= dim <=
+ * EMB_MAX_ROW_DIM, rows < 2^31, eps finite and >= 0. Rows of 16-byte aligned
+ * operands whose dim and strides are multiples of 16 bytes run at the memory's
+ * rate, others element by element. */
+int emb_layer_norm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype, int64_t x_stride, void* y,
+                   int32_t y_dtype, int64_t y_stride, const float* w, const float* b, float eps, void* hip_stream);
+
+/* Its gradient. x is the forward's input, dy (of y_dtype) the gradient of its
+ * output, dx (of x_dtype) receives that of its input, dw and db (fp32 [dim],
+ * overwritten, NULL: not wanted) those of the weights, summed over the rows in
+ * a fixed order (reruns are bit-identical). With h = (x - m) r and g = dy w:
+ *     dx = r (g - mean g - h mean(g h)),  dw = sum of dy h,  db = sum of dy.
+ * dx may be dy or x with the same type and stride. Zero rows give zero dw and
+ * db. ws: device, 16-byte aligned, at least emb_layer_norm_workspace_bytes (0
+ * on invalid arguments and for zero rows). */
+size_t emb_layer_norm_workspace_bytes(int64_t rows, int32_t dim);
+int emb_layer_norm_backward(int64_t rows, int32_t dim, const void* x, int32_t x_dtype, int64_t x_stride,
+                            const void* dy, int32_t y_dtype, int64_t dy_stride, void* dx, int64_t dx_stride,
+                            const float* w, float eps, void* ws, size_t ws_bytes, float* dw, float* db,
+                            void* hip_stream);
+
+/* ---- dropout -------------------------------------------------------------
+ *     y = (kept ? x / (1 - p) : 0) [+ residual]
+ * for each element, 0 <= p <= 1 (1: nothing is kept). The mask is never
+ * stored: it is a function of the element's row and column, the seed and the
+ * step. The gradient of x is the same call, without a residual, on the
+ * gradient of y (and that of the residual is y's gradient itself).
+ * The mask: p is taken as t / 2^32, t = round(p 2^32), in the scale too.
+ * Columns 8 u .. 8 u + 7 of row r take the output of Philox4x32-10 (Salmon,
+ * Moraes, Dror and Shaw, SC 2011) for the key `seed` (low word first) and the
+ * counter (u, r, step mod 2^32, (step / 2^32) mod 2^31): column 8 u + 2 i + h
+ * has bits 16 h .. 16 h + 15 of word i as the upper half, and those of the
+ * output for the last counter word plus 2^31 as the lower half, of a 32-bit
+ * number; it is kept if that is at least t.
+ * step: device int64 [1], read when the kernel runs, so that a captured graph
+ * draws another mask on each replay if the step is counted up in it; NULL: 0.
+ * All operands are of dtype. y may be x or residual with the same stride. What
+ * x holds in dropped places has no influence. dim < 2^31, rows < 2^31. */
+int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
+                int64_t residual_stride, void* y, int64_t y_stride, double p, uint64_t seed, const int64_t* step,
+                void* hip_stream);
+
 #ifdef __cplusplus
 }
 #endif
