@@ -66,7 +66,7 @@ int emb_layer_norm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype, in
 
 size_t emb_layer_norm_workspace_bytes(int64_t rows, int32_t dim) {
   if (check_rows_sizes(rows, dim, EMB_MAX_ROW_DIM)) return 0;
-  return (size_t)layer_norm_back_blocks(rows, dim) * 2 * dim * sizeof(float);
+  return (size_t)layer_norm_back_blocks(rows) * 2 * dim * sizeof(float);
 }
 
 int emb_layer_norm_backward(int64_t rows, int32_t dim, const void* x, int32_t x_dtype, int64_t x_stride,

@@ -169,7 +169,7 @@ struct LayerNormBackArgs {
   float* part;  // [blocks][2][dim]
   float *dw, *db;
 };
-int layer_norm_back_blocks(long long rows, int dim);  // upper bound
+int layer_norm_back_blocks(long long rows);  // upper bound
 hipError_t launch_layer_norm_back(const LayerNormBackArgs& a, hipStream_t st);
 
 struct DropoutArgs {
