@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libemb.so")
 
 SOURCES = ["emb_api.cpp", "emb_plan.cpp", "emb_seq.cpp", "emb_layer.cpp", "k_init.hip", "k_forward.hip", "k_keys_sort.hip", "k_rle.hip",
            "k_reduce.hip", "k_atomic.hip", "k_pack.hip", "k_hash.hip", "k_probe.hip",
-           "k_rotary.hip", "k_prefix.hip", "k_rows.hip"]
+           "k_rotary.hip", "k_prefix.hip", "k_rows.hip",
+           "k_history.hip", "k_history_back.hip", "k_history_step.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

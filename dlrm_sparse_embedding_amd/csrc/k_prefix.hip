@@ -36,55 +36,15 @@
 #include <algorithm>
 #include <cmath>
 
-#include "seq_device.h"
+#include "attn_device.h"
 
 namespace emb {
 
 namespace {
 
-typedef short s4v __attribute__((ext_vector_type(4)));
-typedef short s8v __attribute__((ext_vector_type(8)));
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef _Float16 hf8 __attribute__((ext_vector_type(8)));
-typedef float f16v __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) s4v lds_s4v;
 
 constexpr float kShift = 8.f;  // probabilities carry this many powers of two
 constexpr float kSlack = 7.f;  // and this many more before the reference moves
-constexpr float kNegInf = -__builtin_inff();
-
-template <int DT>
-__device__ __forceinline__ f16v mfma(s8v a, s8v b, f16v c) {
-  if constexpr (DT == EMB_BF16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
-  else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(hf8, a), __builtin_bit_cast(hf8, b), c, 0, 0, 0);
-}
-
-template <int DT>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  const fl2 f = {x, y};
-  if constexpr (DT == EMB_BF16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf2));
-  else return __builtin_bit_cast(uint32_t, __builtin_convertvector(f, hf2));
-}
-
-// A row's two lanes (l and l + 32) joined.
-__device__ __forceinline__ void halves(float x, float* lo, float* hi) {
-  typedef unsigned u2v __attribute__((ext_vector_type(2)));
-  const u2v r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  *lo = __uint_as_float(r.x);
-  *hi = __uint_as_float(r.y);
-}
-__device__ __forceinline__ float both_halves_max(float x) {
-  float lo, hi;
-  halves(x, &lo, &hi);
-  return fmaxf(lo, hi);
-}
-__device__ __forceinline__ float both_halves_sum(float x) {
-  float lo, hi;
-  halves(x, &lo, &hi);
-  return lo + hi;
-}
 
 struct PrefixDev {
   PrefixArgs a;
@@ -114,25 +74,6 @@ __device__ __forceinline__ int first_token(const PrefixDev& p, int b) {
 __device__ __forceinline__ int group_token(const PrefixDev& p, int g) {
   const int b = p.a.group_offsets[g];
   return first_token(p, min(max(b, 0), p.a.seqs));
-}
-
-// The last i in [0, n) with f(i) <= x, f non-decreasing, by one wave: 64
-// places at a time.
-template <class F>
-__device__ __forceinline__ int wave_find(int n, int x, F f) {
-  const int lane = threadIdx.x & 63;
-  int lo = 0, len = n;
-  while (len > 1) {
-    const int step = (len + 63) >> 6;
-    const int i = lo + lane * step;
-    const bool le = lane * step < len && f(i) <= x;
-    const uint64_t mask = __ballot(le);
-    const int k = mask ? 63 - __clzll(mask) : 0;
-    const int at = k * step;
-    len = min(step, len - at);
-    lo += at;
-  }
-  return lo;
 }
 
 // What one wave works on: 32 rows of cache head `h` and the slots [k0, k1) of
@@ -219,16 +160,6 @@ __device__ __forceinline__ s8v read_vt(const short* v, int kk, int d0) {
   return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-template <int N>
-__device__ __forceinline__ float top_of(const f16v (&s)[N]) {
-  float top = s[0][0];
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int i = n == 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
-  return top;
-}
-
 // Takes N tiles' scores (raw products) into the running maximum. The outputs
 // are rescaled only where a maximum has grown by more than kSlack since the
 // reference was set: any reference gives the same quotient, and the slack
@@ -271,14 +202,6 @@ __device__ __forceinline__ void probabilities(const PrefixDev& p, Wave<DT, D>& w
     prob[k] = __builtin_bit_cast(s8v, b);
   }
   w.sum += sum;
-}
-
-// Clears the scores of a tile's slots at and beyond `seen` (the lane's own limit).
-__device__ __forceinline__ void mask_tile(f16v& s, int slot0, int seen) {
-  const int h4 = 4 * ((threadIdx.x & 63) >> 5);
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (slot0 + 8 * (i / 4) + h4 + i % 4 >= seen) s[i] = kNegInf;
 }
 
 // The keys of slot lane % 32 of a tile, and the values of the lane's pieces,

@@ -183,8 +183,69 @@ struct DropoutArgs {
 };
 hipError_t launch_dropout(const DropoutArgs& a, hipStream_t st);
 
+// ---- attention of histories (k_history.hip, k_history_back.hip, k_history_step.hip) ----
+// Buckets of distances d >= 0: d below `exact`, then those that start at
+// first[exact] = exact, .., first[buckets - 1]; first[buckets] is 2^31 - 1.
+struct Buckets {
+  int n, exact;             // n = 0: no bias
+  int first[EMB_MAX_BUCKETS + 1];
+  float log2_exact, slope;  // the bucket is exact + (log2 d - log2_exact) * slope, to within one
+};
+
+struct HistoryView {
+  int q_heads, kv_heads, dim, dtype, causal;
+  float scale;
+  Buckets buckets;
+  int* error;  // may be null
+};
+
+struct HistoryArgs {
+  HistoryView h;
+  int tokens, seqs;
+  Heads q, k, v, out;  // out.p is written by the forward
+  const int* offsets;
+  const float* bias;  // null where there are no buckets
+  float* lse;         // may be null in the forward
+};
+hipError_t launch_history(const HistoryArgs& a, hipStream_t st);
+
+struct HistoryBackArgs {
+  HistoryArgs f;
+  Heads dout, dq, dk, dv;
+  float* dbias;  // may be null
+  float* rows;   // workspace: [q_heads][tokens] sums P dP
+  float* part;   // workspace: [blocks][rows of the bias] partial sums of dbias
+};
+// What the workspace holds (bytes): the rows' sums, then the partial sums.
+struct HistoryBackPlan {
+  size_t part_off, bytes;
+};
+HistoryBackPlan history_back_plan(const HistoryView& h, long long tokens, int seqs);
+hipError_t launch_history_back(const HistoryBackArgs& a, hipStream_t st);
+
+struct HistoryStepArgs {
+  HistoryView h;
+  KvView kv;
+  int seqs;
+  Heads q, out;
+  const int* lens;
+  const int* table;
+  int width;
+  const float* bias;
+  float* lse;
+  int parts;
+  float* part_o;    // [parts][seqs][q_heads][dim]
+  float* part_lse;  // [parts][seqs][q_heads]
+};
+int history_step_parts(const HistoryView& h, const KvView& kv, int seqs, int width);
+hipError_t launch_history_step(const HistoryStepArgs& a, hipStream_t st);
+
 }  // namespace emb
 
 struct emb_kv {
   emb::KvView v;
+};
+
+struct emb_history {
+  emb::HistoryView v;
 };

@@ -96,6 +96,17 @@ class emb_kv_desc(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("error", ctypes.c_void_p)]
 
 
+EMB_MAX_ROW_DIM = 16384
+EMB_MAX_BUCKETS = 128
+
+
+class emb_history_desc(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("causal", ctypes.c_int32), ("buckets", ctypes.c_int32),
+                ("exact", ctypes.c_int32), ("far", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("error", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -200,6 +211,23 @@ def lib() -> ctypes.CDLL:
     L.emb_layer_norm_workspace_bytes.restype = sz
     L.emb_layer_norm_backward.argtypes = [i64, i32] + rows_io * 2 + [vp, i64, vp, f32, vp, sz, vp, vp, vp]
     L.emb_layer_norm_backward.restype = ctypes.c_int
+    L.emb_create_history.argtypes = [ctypes.POINTER(emb_history_desc), ctypes.POINTER(vp)]
+    L.emb_create_history.restype = ctypes.c_int
+    L.emb_destroy_history.argtypes = [vp]
+    L.emb_destroy_history.restype = None
+    L.emb_check_history_error.argtypes = [vp, vp]
+    L.emb_check_history_error.restype = ctypes.c_int
+    L.emb_history_attention.argtypes = [vp, i64] + heads_io * 4 + [vp, i32, vp, vp, vp]
+    L.emb_history_attention.restype = ctypes.c_int
+    L.emb_history_attention_workspace_bytes.argtypes = [vp, i64, i32]
+    L.emb_history_attention_workspace_bytes.restype = sz
+    L.emb_history_attention_backward.argtypes = ([vp, i64] + heads_io * 4 + [vp] + heads_io * 4 +
+                                                 [vp, i32, vp, vp, sz, vp, vp])
+    L.emb_history_attention_backward.restype = ctypes.c_int
+    L.emb_history_step_workspace_bytes.argtypes = [vp, vp, i32, i32]
+    L.emb_history_step_workspace_bytes.restype = sz
+    L.emb_history_step.argtypes = [vp, vp, i32] + heads_io * 2 + [vp, vp, i32, vp, vp, sz, vp, vp]
+    L.emb_history_step.restype = ctypes.c_int
     L.emb_dropout.argtypes = [i64, i32, i32] + [vp, i64] * 3 + [ctypes.c_double, ctypes.c_uint64, vp, vp]
     L.emb_dropout.restype = ctypes.c_int
     _lib = L
@@ -668,6 +696,101 @@ def emb_dropout(x, y, p: float, seed: int, step=None, residual=None, stream=None
                              _stream_for(x, stream)))
 
 
+def emb_create_history(desc: emb_history_desc) -> int:
+    out = ctypes.c_void_p()
+    _check(lib().emb_create_history(ctypes.byref(desc), ctypes.byref(out)))
+    return out.value
+
+
+def emb_destroy_history(history: int) -> None:
+    lib().emb_destroy_history(history)
+
+
+def emb_check_history_error(history: int, stream=None) -> None:
+    _check(lib().emb_check_history_error(history, _stream(stream)))
+
+
+def _ragged(q, k, v, history_dims):
+    """Checks the heads of a call on ragged histories (a HistoryAttention's); the operands' arguments."""
+    hq, hk, D, dtype = history_dims
+    T = q.shape[0]
+    for name, t, n in (("q", q, hq), ("k", k, hk), ("v", v, hk)):
+        if t.dim() != 3 or t.shape[1] != n:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, not [{T}, {n}, {D}]")
+    return T, [*_heads("q", q, T, D, dtype), *_heads("k", k, T, D, dtype), *_heads("v", v, T, D, dtype)]
+
+
+def _like(name: str, t, like):
+    """Checks that a [tokens, heads, dim] operand has another's shape and type; its arguments."""
+    if t.shape != like.shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(like.shape)}")
+    return _heads(name, t, like.shape[0], like.shape[2], like.dtype)
+
+
+def _offsets(offsets):
+    if offsets.dim() != 1 or offsets.shape[0] < 1:
+        raise ValueError("offsets must be [seqs + 1]")
+    return _dense("offsets", offsets, torch.int32, offsets.shape), offsets.shape[0] - 1
+
+
+# What a handle stands for, so that operands can be checked: q heads, k heads, dim, type, rows of the bias.
+_histories = {}
+
+
+def _bias(name: str, bias, dims):
+    return None if bias is None else _dense(name, bias, torch.float32, (dims[4], dims[0]))
+
+
+def emb_history_attention(history: int, q, k, v, out, offsets, bias=None, lse=None, stream=None) -> None:
+    """q, out: [tokens, q_heads, dim]; k, v: [tokens, kv_heads, dim]; offsets: int32 [seqs + 1]; bias: fp32 [rows,
+    q_heads], given if and only if the history has buckets; lse: fp32 [tokens, q_heads] or None."""
+    dims = _histories[history]
+    T, args = _ragged(q, k, v, dims[:4])
+    off, B = _offsets(offsets)
+    _check(lib().emb_history_attention(
+        history, T, *args, *_like("out", out, q), off, B, _bias("bias", bias, dims),
+        None if lse is None else _dense("lse", lse, torch.float32, (T, dims[0])), _stream_for(q, stream)))
+
+
+def emb_history_attention_workspace_bytes(history: int, tokens: int, seqs: int) -> int:
+    return int(lib().emb_history_attention_workspace_bytes(history, int(tokens), int(seqs)))
+
+
+def emb_history_attention_backward(history: int, q, k, v, out, lse, dout, dq, dk, dv, offsets, ws, bias=None,
+                                   dbias=None, stream=None) -> None:
+    """Gradients of emb_history_attention from its inputs, out and lse: dq, dk, dv and, where given, dbias."""
+    dims = _histories[history]
+    T, args = _ragged(q, k, v, dims[:4])
+    off, B = _offsets(offsets)
+    ws_p, ws_n = _workspace(ws)
+    _check(lib().emb_history_attention_backward(
+        history, T, *args, *_like("out", out, q), _dense("lse", lse, torch.float32, (T, dims[0])),
+        *_like("dout", dout, q), *_like("dq", dq, q), *_like("dk", dk, k), *_like("dv", dv, v), off, B,
+        _bias("bias", bias, dims), ws_p, ws_n, _bias("dbias", dbias, dims), _stream_for(q, stream)))
+
+
+def emb_history_step_workspace_bytes(history: int, kv: int, seqs: int, table_width: int) -> int:
+    return int(lib().emb_history_step_workspace_bytes(history, kv, int(seqs), int(table_width)))
+
+
+def emb_history_step(history: int, kv: int, q, out, lens, table, ws, bias=None, lse=None, stream=None) -> None:
+    """q, out: [seqs, q_heads, dim], a query for each sequence at its newest slot; lens: int32 [seqs]; table: int32
+    [seqs, pages]."""
+    dims = _histories[history]
+    hq, _, D, dtype, _ = dims
+    if q.dim() != 3 or q.shape[1] != hq:
+        raise ValueError(f"q has shape {tuple(q.shape)}, not [seqs, {hq}, {D}]")
+    B = q.shape[0]
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs, pages]")
+    width = table.shape[1]
+    ws_p, ws_n = _workspace(ws)
+    _check(lib().emb_history_step(
+        history, kv, B, *_heads("q", q, B, D, dtype), *_like("out", out, q), _dense("lens", lens, torch.int32, (B,)),
+        _dense("table", table, torch.int32, (B, width)), width, _bias("bias", bias, dims), ws_p, ws_n,
+        None if lse is None else _dense("lse", lse, torch.float32, (B, hq)), _stream_for(q, stream)))
+
+
 class Rotary:
     """A rotation: the first `rot` elements of each head, in the "half" or "interleaved" layout, with the
     frequencies of `base`, scaled by one of "none", "linear", "base", "parts" and "bands" (include/emb.h)."""
@@ -726,6 +849,39 @@ class KVCache:
     def check_error(self, stream=None) -> None:
         """Waits for the stream; raises if a call met a bad page, length or offset since the last check."""
         emb_check_kv_error(self.handle, stream)
+
+
+class HistoryAttention:
+    """The attention of ragged histories: heads of `dim` elements of "bf16" or "f16", `scale` (1 / sqrt(dim) by
+    default), and a bias by relative position with `buckets` buckets, of which the first `exact` hold one distance
+    each and the last one starts near `far` (0 buckets: no bias; include/emb.h). `bias_rows` is the number of rows of
+    its table, fp32 [bias_rows, q_heads]."""
+
+    def __init__(self, q_heads: int, kv_heads: int, dim: int, dtype: str = "bf16", scale: float | None = None,
+                 causal: bool = True, buckets: int = 0, exact: int = 0, far: int = 0, device="cuda"):
+        self.handle = None
+        self.error = torch.zeros(1, dtype=torch.int32, device=device)
+        scale = dim ** -0.5 if scale is None else scale
+        self.handle = emb_create_history(emb_history_desc(q_heads, kv_heads, dim, DTYPE_CODE[dtype], 1 if causal else 0,
+                                                          buckets, exact, far, scale, 0, self.error.data_ptr()))
+        self.bias_rows = buckets if causal else 2 * buckets
+        _histories[self.handle] = (q_heads, kv_heads, dim, TORCH_DTYPE[dtype], self.bias_rows)
+
+    def close(self) -> None:
+        if self.handle:
+            _histories.pop(self.handle, None)
+            emb_destroy_history(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def check_error(self, stream=None) -> None:
+        """Waits for the stream; raises if a call met offsets that break their contract since the last check."""
+        emb_check_history_error(self.handle, stream)
 
 
 # ---- convenience: a context with the tensors behind it ---------------------

@@ -659,8 +659,11 @@ int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim,
 
 /* ======================================================================
  * History layer: what trains a layer over users' histories, next to the
- * operators above. Layer norm with its gradient, and dropout. The conventions
- * are those of the sequence operators.
+ * operators above, and serves it. Layer norm with its gradient, dropout, and
+ * the attention of a ragged batch of histories over themselves with a learned
+ * bias by relative position, its gradient, and its form for one new item of
+ * each history over the paged cache. The conventions are those of the
+ * sequence operators.
  *
  * A "rows" operand is [rows][dim] in device memory, given as a pointer and a
  * row stride in elements; the dim elements of a row are contiguous. Operands
@@ -717,6 +720,106 @@ int emb_layer_norm_backward(int64_t rows, int32_t dim, const void* x, int32_t x_
 int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t x_stride, const void* residual,
                 int64_t residual_stride, void* y, int64_t y_stride, double p, uint64_t seed, const int64_t* step,
                 void* hip_stream);
+
+/* ---- attention of histories with a bias by relative position ---------------
+ * A batch of sequences ("histories") of unlike lengths without padding:
+ * sequence b's tokens are offsets[b] .. offsets[b+1] of the operands (int32
+ * [seqs+1], offsets[0] = 0, non-decreasing, offsets[seqs] = tokens; empty
+ * sequences are allowed). With i and j places in one sequence,
+ *     s_ij = scale q_i . k_j + bias[row(i - j)][head],
+ *     out_i = sum_j softmax_j(s_ij) v_j,  lse_i = ln sum_j exp(s_ij)
+ * over j <= i (causal != 0) or all j of the sequence (causal = 0). Query head h
+ * reads key head h / (q_heads / kv_heads).
+ * The bias is an fp32 table [rows][q_heads] with a row for each bucket of
+ * distances. bucket(d) = d below `exact`; from there on bucket exact + k starts
+ * at the smallest whole d >= exact (far / exact)^(k / (buckets - exact)), so
+ * buckets widen evenly on a logarithmic scale and the last one holds all
+ * distances from near `far` on. row(d) = bucket(d) for d >= 0 and, without
+ * causal, buckets + bucket(-d) for d < 0, so the table has `buckets` rows or 2
+ * buckets (row `buckets` is then never used). exact = buckets: distances beyond
+ * buckets - 1 share the last bucket, far is not used. buckets = 0: no bias.
+ * An entry at or below -2^100 (-infinity, the type's lowest value) hides its
+ * distances: their keys are not seen. A query that sees no key gets zeros and
+ * -infinity, and its gradients are zeros. Other entries and the scores must
+ * stay below 2^100 in magnitude.
+ * Tokens that a query does not see have no influence on its row, whatever they
+ * hold (other sequences', later ones'), except that hidden keys' infinities
+ * enter products with a weight of 0. Reruns are bit-identical.
+ * EMB_BF16 / EMB_F16 heads of dim 64, 96 or 128; operands 16-byte aligned, their
+ * strides multiples of 16 bytes. Softmax statistics, scores and sums are fp32;
+ * probabilities and score gradients are rounded to the heads' type for the
+ * matrix products (fp16 ones are scaled by powers of two first). */
+typedef struct emb_history_desc {
+  int32_t q_heads;    /* 1..64 times kv_heads, < 65536 */
+  int32_t kv_heads;   /* >= 1 */
+  int32_t dim;        /* 64, 96, 128 */
+  int32_t dtype;      /* EMB_BF16 | EMB_F16 */
+  int32_t causal;
+  int32_t buckets;    /* 0..EMB_MAX_BUCKETS */
+  int32_t exact;      /* 1..buckets (0 if buckets is 0) */
+  int32_t far;        /* exact+1 .. 2^30 where exact < buckets */
+  float   scale;      /* 2^-100 .. 2^100 */
+  int32_t reserved;   /* must be 0 */
+  int32_t* error;     /* device int32, set to 0 by the caller; NULL: no reports */
+} emb_history_desc;
+
+#define EMB_MAX_BUCKETS 128
+
+typedef struct emb_history emb_history;
+
+/* Computes the buckets' bounds on the host. Touches no device. */
+int emb_create_history(const emb_history_desc* desc, emb_history** out);
+void emb_destroy_history(emb_history* history);
+
+/* Synchronises the stream, reads and clears the error flag: EMB_E_INVAL if a
+ * call met offsets that break their contract (its results are unspecified; no
+ * access leaves the operands), else EMB_OK (always without an error word). */
+int emb_check_history_error(emb_history* history, void* hip_stream);
+
+/* q, out: [tokens][q_heads][dim]; k, v: [tokens][kv_heads][dim]; lse: fp32
+ * [tokens][q_heads] or NULL (the gradient needs it). bias: NULL if and only if
+ * buckets is 0; 4-byte aligned, like lse. tokens < 2^24, seqs < 2^24. */
+int emb_history_attention(emb_history* history, int64_t tokens, const void* q, int64_t q_token_stride,
+                          int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                          const void* v, int64_t v_token_stride, int64_t v_head_stride, void* out,
+                          int64_t out_token_stride, int64_t out_head_stride, const int32_t* offsets, int32_t seqs,
+                          const float* bias, float* lse, void* hip_stream);
+
+/* The gradient: from the forward's inputs, its out and lse and the gradient
+ * dout of out, those of q, k, v and of the bias (dbias: fp32 [rows][q_heads],
+ * overwritten, summed in a fixed order; NULL: not wanted). With dP = dout . v
+ * and dS = P (dP - sum_j P dP): dq = scale dS k, dk = scale dS^T q, dv = P^T
+ * dout, dbias = the sums of dS over each bucket. ws: device, 16-byte aligned,
+ * at least emb_history_attention_workspace_bytes (0 on invalid arguments). */
+size_t emb_history_attention_workspace_bytes(const emb_history* history, int64_t tokens, int32_t seqs);
+int emb_history_attention_backward(emb_history* history, int64_t tokens, const void* q, int64_t q_token_stride,
+                                   int64_t q_head_stride, const void* k, int64_t k_token_stride,
+                                   int64_t k_head_stride, const void* v, int64_t v_token_stride,
+                                   int64_t v_head_stride, const void* out, int64_t out_token_stride,
+                                   int64_t out_head_stride, const float* lse, const void* dout,
+                                   int64_t dout_token_stride, int64_t dout_head_stride, void* dq,
+                                   int64_t dq_token_stride, int64_t dq_head_stride, void* dk,
+                                   int64_t dk_token_stride, int64_t dk_head_stride, void* dv,
+                                   int64_t dv_token_stride, int64_t dv_head_stride, const int32_t* offsets,
+                                   int32_t seqs, const float* bias, void* ws, size_t ws_bytes, float* dbias,
+                                   void* hip_stream);
+
+/* Serving: one query for each sequence of a cache (of the same kv_heads, dim
+ * and dtype, 16-byte aligned, strides multiples of 16 bytes), at the place of
+ * its newest slot: q and out are [seqs][q_heads][dim], sequence b's query sees
+ * its slots 0 .. lens[b] - 1 of table[b] (int32 [seqs][table_width], as
+ * emb_kv_append), slot j at distance lens[b] - 1 - j. lens[b] = 0: zeros and
+ * -infinity. Bad pages and lengths raise the cache's error flag; table_width
+ * bounds the split of the work, so it should not be much wider than needed.
+ * q_heads is at most 32 times kv_heads. lse: fp32 [seqs][q_heads] or NULL. ws:
+ * device, 16-byte aligned, at least emb_history_step_workspace_bytes (0 on
+ * invalid arguments). */
+size_t emb_history_step_workspace_bytes(const emb_history* history, const emb_kv* kv, int32_t seqs,
+                                        int32_t table_width);
+int emb_history_step(emb_history* history, emb_kv* kv, int32_t seqs, const void* q, int64_t q_token_stride,
+                     int64_t q_head_stride, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                     const int32_t* lens, const int32_t* table, int32_t table_width, const float* bias, void* ws,
+                     size_t ws_bytes, float* lse, void* hip_stream);
 
 #ifdef __cplusplus
 }

@@ -1,4 +1,4 @@
-"""Refusals of layer norm and dropout (CPU): every bad call is turned away with its status code and a message before
+"""Refusals of the history layer (CPU): every bad call is turned away with its status code and a message before
 anything reaches the device. The C entry points are called with made-up addresses that are never dereferenced."""
 import math
 
@@ -89,3 +89,141 @@ def test_binding_checks_shapes_and_types():
         E.emb_layer_norm(x, x, None, None, 0.0)               # not in device memory
     with pytest.raises(ValueError):
         E.emb_dropout(x.double(), x, 0.1, 0)
+
+
+# ---- attention of histories ---------------------------------------------------------
+
+DESC = dict(hq=8, hk=2, dim=64, t=E.EMB_BF16, causal=1, buckets=32, exact=16, far=128, scale=0.125, reserved=0, error=None)
+
+
+def history_rc(**kw):
+    f = dict(DESC)
+    f.update(kw)
+    out = E.ctypes.c_void_p()
+    rc = E.lib().emb_create_history(E.emb_history_desc(*f.values()), out)
+    if rc == OK:
+        E.emb_destroy_history(out)
+    else:
+        assert out.value is None and E.lib().emb_last_error()
+    return rc
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(t=E.EMB_F32), DTYPE), (dict(t=9), DTYPE), (dict(dim=32), INVAL), (dict(dim=256), INVAL), (dict(hk=0), INVAL),
+    (dict(hq=0), INVAL), (dict(hq=7), INVAL), (dict(hq=130), INVAL), (dict(hq=65536, hk=65536), INVAL),
+    (dict(scale=0.0), INVAL), (dict(scale=-1.0), INVAL), (dict(scale=math.nan), INVAL), (dict(scale=math.inf), INVAL),
+    (dict(buckets=-1), INVAL), (dict(buckets=129), INVAL), (dict(exact=0), INVAL), (dict(exact=33), INVAL),
+    (dict(far=16), INVAL), (dict(far=(1 << 30) + 1), INVAL), (dict(buckets=0), INVAL), (dict(reserved=1), INVAL),
+    (dict(error=FAKE + 2), INVAL),
+])
+def test_history_descriptor_rejects(kw, code):
+    assert history_rc(**kw) == code
+
+
+def test_history_descriptor_accepts():
+    assert history_rc() == OK
+    assert history_rc(buckets=0, exact=0, far=0) == OK
+    assert history_rc(buckets=128, exact=128, far=0, causal=0) == OK
+    assert history_rc(buckets=128, exact=1, far=1 << 30) == OK
+    E.lib().emb_destroy_history(None)
+    assert E.lib().emb_create_history(None, None) == INVAL
+
+
+def handle(**kw):
+    f = dict(DESC)
+    f.update(kw)
+    return E.emb_create_history(E.emb_history_desc(*f.values()))
+
+
+def cache(dim=64, heads=2, dtype=E.EMB_BF16, k=FAKE, slot=64):
+    return E.emb_create_kv(E.emb_kv_desc(k, FAKE, 16 * heads * dim, slot, 16 * dim, 16 * heads * dim, slot, 16 * dim,
+                                         100, 16, heads, dim, dtype, None))
+
+
+ATT = dict(h=None, tokens=10, q=FAKE, qts=768, qhs=64, k=FAKE, kts=768, khs=64, v=FAKE, vts=768, vhs=64, out=FAKE,
+           ots=512, ohs=64, off=FAKE, seqs=2, bias=FAKE, lse=FAKE, st=None)
+BAD_RAGGED = [
+    dict(h=0), dict(tokens=-1), dict(tokens=1 << 24), dict(seqs=-1), dict(seqs=0), dict(seqs=1 << 24), dict(bias=None),
+    dict(bias=FAKE + 2), dict(off=None), dict(off=FAKE + 2), dict(q=None), dict(q=FAKE + 8), dict(k=FAKE + 2),
+    dict(v=None), dict(qts=764), dict(khs=60), dict(vts=-768), dict(kts=1 << 24),
+]
+
+
+@pytest.mark.parametrize("kw", BAD_RAGGED + [dict(out=None), dict(ots=448), dict(ohs=32), dict(lse=FAKE + 2)])
+def test_history_attention_rejects(kw):
+    h = handle()
+    assert rc_of("emb_history_attention", dict(ATT, h=h), {k: (None if k == "h" else v) for k, v in kw.items()}) == INVAL
+    E.emb_destroy_history(h)
+
+
+def test_history_attention_without_buckets_or_tokens():
+    h, plain = handle(), handle(buckets=0, exact=0, far=0)
+    assert rc_of("emb_history_attention", dict(ATT, h=plain), {}) == INVAL          # a bias without buckets
+    assert rc_of("emb_history_attention", dict(ATT, h=h), dict(tokens=0, seqs=0, q=None, off=None)) == OK
+    assert E.lib().emb_check_history_error(h, None) == OK and E.lib().emb_check_history_error(None, None) == INVAL
+    for x in (h, plain):
+        E.emb_destroy_history(x)
+
+
+BACK_ATT = dict(h=None, tokens=10, q=FAKE, qts=768, qhs=64, k=FAKE, kts=768, khs=64, v=FAKE, vts=768, vhs=64, out=FAKE,
+                ots=512, ohs=64, lse=FAKE, dout=FAKE, gts=512, ghs=64, dq=FAKE, dqts=512, dqhs=64, dk=FAKE, dkts=128,
+                dkhs=64, dv=FAKE, dvts=128, dvhs=64, off=FAKE, seqs=2, bias=FAKE, ws=FAKE, n=1 << 20, dbias=FAKE, st=None)
+
+
+@pytest.mark.parametrize("kw,code", [(k, INVAL) for k in BAD_RAGGED] + [
+    (dict(lse=None), INVAL), (dict(lse=FAKE + 1), INVAL), (dict(dout=None), INVAL), (dict(gts=1 << 24), INVAL),
+    (dict(dq=None), INVAL), (dict(dk=FAKE + 8), INVAL), (dict(dvts=64), INVAL), (dict(dkhs=32), INVAL),
+    (dict(ws=None), INVAL), (dict(ws=FAKE + 8), INVAL), (dict(n=100), WS), (dict(dbias=FAKE + 2), INVAL),
+])
+def test_history_backward_rejects(kw, code):
+    h = handle()
+    kw = {k: (None if k == "h" else v) for k, v in kw.items()}
+    assert rc_of("emb_history_attention_backward", dict(BACK_ATT, h=h), kw) == code
+    E.emb_destroy_history(h)
+
+
+def test_history_workspaces():
+    h, kv = handle(), cache()
+    f = E.emb_history_attention_workspace_bytes
+    assert f(h, 1000, 4) >= 1000 * 8 * 4 and f(h, -1, 4) == 0 and f(h, 10, -1) == 0
+    assert E.emb_history_step_workspace_bytes(h, kv, 4, 100) >= 16
+    assert E.emb_history_step_workspace_bytes(h, kv, -1, 100) == 0
+    E.emb_destroy_history(h)
+    E.emb_destroy_kv(kv)
+
+
+STEP = dict(h=None, kv=None, seqs=4, q=FAKE, qts=512, qhs=64, out=FAKE, ots=512, ohs=64, lens=FAKE, table=FAKE, width=8,
+            bias=FAKE, ws=FAKE, n=1 << 24, lse=FAKE, st=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(h=0), INVAL), (dict(kv=0), INVAL), (dict(seqs=-1), INVAL), (dict(seqs=1 << 24), INVAL), (dict(q=None), INVAL),
+    (dict(q=FAKE + 8), INVAL), (dict(qts=508), INVAL), (dict(out=None), INVAL), (dict(ots=448), INVAL),
+    (dict(lens=None), INVAL), (dict(lens=FAKE + 2), INVAL), (dict(table=None), INVAL), (dict(width=-1), INVAL),
+    (dict(width=1 << 27), INVAL), (dict(bias=None), INVAL), (dict(bias=FAKE + 1), INVAL), (dict(lse=FAKE + 3), INVAL),
+    (dict(ws=None), INVAL), (dict(ws=FAKE + 4), INVAL), (dict(n=8), WS),
+])
+def test_history_step_rejects(kw, code):
+    h, kv = handle(), cache()
+    kw = {k: (None if k in ("h", "kv") else v) for k, v in kw.items()}
+    assert rc_of("emb_history_step", dict(STEP, h=h, kv=kv), kw) == code
+    E.emb_destroy_history(h)
+    E.emb_destroy_kv(kv)
+
+
+@pytest.mark.parametrize("desc,kv,code", [
+    (dict(), dict(dim=128), INVAL), (dict(), dict(heads=4), INVAL), (dict(), dict(dtype=E.EMB_F16), DTYPE),
+    (dict(), dict(k=FAKE + 2), INVAL), (dict(), dict(slot=68), INVAL), (dict(hq=66, hk=2), dict(), INVAL),
+])
+def test_history_step_rejects_caches_that_do_not_fit(desc, kv, code):
+    h, c = handle(**desc), cache(**kv)
+    assert rc_of("emb_history_step", dict(STEP, h=h, kv=c), {}) == code
+    E.emb_destroy_history(h)
+    E.emb_destroy_kv(c)
+
+
+def test_history_step_without_sequences():
+    h, c = handle(), cache()
+    assert rc_of("emb_history_step", dict(STEP, h=h, kv=c), dict(seqs=0, q=None, lens=None, ws=None)) == OK
+    E.emb_destroy_history(h)
+    E.emb_destroy_kv(c)
