@@ -110,7 +110,7 @@ int check_ragged(const emb_history* h, int64_t tokens, const int32_t* offsets, i
   if (tokens < 0 || tokens >= (1ll << 24)) return fail(EMB_E_INVAL, "tokens %lld not in [0, 2^24)", (long long)tokens);
   if (seqs < 0 || seqs >= (1 << 24)) return fail(EMB_E_INVAL, "seqs %d not in [0, 2^24)", seqs);
   if (seqs == 0 && tokens > 0) return fail(EMB_E_INVAL, "tokens without a sequence");
-  if ((seqs + tokens / 128) * h->v.q_heads >= (1ll << 30) || tokens * h->v.q_heads >= (1ll << 31))
+  if ((seqs + tokens / 64) * h->v.q_heads >= (1ll << 30) || tokens * h->v.q_heads >= (1ll << 31))
     return fail(EMB_E_INVAL, "too many tokens or sequences for one call");
   if (h->v.buckets.n > 0 && (!bias || !aligned(bias, 4))) return fail(EMB_E_INVAL, "bias is NULL or misaligned");
   if (h->v.buckets.n == 0 && bias) return fail(EMB_E_INVAL, "bias without buckets");

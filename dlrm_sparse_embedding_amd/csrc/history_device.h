@@ -24,29 +24,47 @@ __device__ __forceinline__ int swizzle(int r) {
   else return (r >> 2) & 3;
 }
 
-// Operand of rows row0 + lane % 32, contracted over their elements 16 i .. + 15.
+// Where a lane reads in a tile, as byte offsets: of its row's operands and of its
+// columns' two halves. The 16-byte pieces of a row are a power of two (D = 64,
+// 128), so that an operand's piece is one exclusive or away; for D = 96 their
+// lowest two bits are swizzled and two offsets are kept.
 template <int D>
-__device__ __forceinline__ s8v row_operand(const short* tile, int row0, int i) {
-  const int lane = threadIdx.x & 63, r = lane & 31;
-  return *reinterpret_cast<const s8v*>(tile + (row0 + r) * D + 8 * ((2 * i + (lane >> 5)) ^ swizzle<D>(r)));
-}
-// Operand of the tile's columns 32 d + lane % 32, contracted over the 16 rows
-// from row0 on, in the order that a product's elements 8 k .. 8 k + 7 have.
-template <int D>
-__device__ __forceinline__ s8v column_operand(const short* tile, int row0, int d, int lane) {
-  const int q = lane & 15;
-  const int r = 4 * (lane >> 5) + (q >> 2);
-  const int c = (4 * d + 2 * ((lane >> 4) & 1) + ((q & 3) >> 1)) ^ swizzle<D>(r);
-  const short* at = tile + (row0 + r) * D + 4 * (q & 1);
-  const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * c));
-  const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + 8 * D + 8 * (c ^ 2)));  // swizzle(r + 8)
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-template <int D>
-__device__ __forceinline__ s8v column_operand(const short* tile, int row0, int d) {
-  return column_operand<D>(tile, row0, d, threadIdx.x & 63);
-}
+struct TileLane {
+  uint32_t row[D == 96 ? 2 : 1], col[2];
+  __device__ __forceinline__ TileLane() : TileLane(threadIdx.x & 63) {}
+  __device__ __forceinline__ explicit TileLane(int lane) {
+    const int r = lane & 31, h = lane >> 5;
+    row[0] = 2 * D * r + 16 * (h ^ swizzle<D>(r));
+    if constexpr (D == 96) row[1] = 2 * D * r + 16 * ((2 + h) ^ swizzle<D>(r));
+    const int q = lane & 15, cr = 4 * h + (q >> 2);
+    const int c = (2 * ((lane >> 4) & 1) + ((q & 3) >> 1)) ^ swizzle<D>(cr);
+    col[0] = 2 * D * cr + 8 * (q & 1) + 16 * c;
+    col[1] = 2 * D * (cr + 8) + 8 * (q & 1) + 16 * (c ^ 2);  // swizzle(r + 8) = swizzle(r) ^ 2
+  }
+  // Offsets that the compiler takes as new: what is worked out from them is not
+  // held in registers beyond this point.
+  __device__ __forceinline__ TileLane fresh() const {
+    TileLane t = *this;
+#pragma unroll
+    for (uint32_t& x : t.row) asm volatile("" : "+v"(x));
+    asm volatile("" : "+v"(t.col[0]), "+v"(t.col[1]));
+    return t;
+  }
+  // Operand of the tile's rows row0 + lane % 32, contracted over their elements 16 i .. + 15.
+  __device__ __forceinline__ s8v rows(const short* tile, int row0, int i) const {
+    const uint32_t at = D == 96 ? row[(i & 1) * (D == 96)] + 64 * (i / 2) : row[0] ^ (32 * i);
+    return *reinterpret_cast<const s8v*>(reinterpret_cast<const char*>(tile) + 2 * D * row0 + at);
+  }
+  // Operand of the tile's columns 32 d + lane % 32, contracted over the 16 rows
+  // from row0 on, in the order that a product's elements 8 k .. 8 k + 7 have.
+  __device__ __forceinline__ s8v columns(const short* tile, int row0, int d) const {
+    const uint32_t a = D == 96 ? col[0] + 64 * d : col[0] ^ (64 * d), b = D == 96 ? col[1] + 64 * d : col[1] ^ (64 * d);
+    const char* at = reinterpret_cast<const char*>(tile) + 2 * D * row0;
+    const s4v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + a));
+    const s4v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4v*)(at + b));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+};
 
 typedef __attribute__((address_space(3))) short lds_elem;
 
@@ -62,6 +80,15 @@ __device__ __forceinline__ void fetch_to_lds(uint64_t base, uint32_t off, uint32
                : "{m0}"(at), "v"(off), "s"(base)
                : "memory");
 }
+// The same with 4 bytes a lane.
+__device__ __forceinline__ void fetch_word_to_lds(uint64_t base, uint32_t off, uint32_t at) {
+  uint64_t from;
+  asm volatile("s_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+               : "=&s"(from)
+               : "{m0}"(at), "v"(off), "s"(base)
+               : "memory");
+}
+typedef __attribute__((address_space(3))) float lds_word;
 __device__ __forceinline__ void fetched() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ uint64_t uniform(uint64_t x) {
@@ -72,25 +99,28 @@ __device__ __forceinline__ uint64_t uniform(uint64_t x) {
 // The fetches of a block of 256 threads: 64 rows are D / 32 for each thread.
 template <int D>
 struct RowFetch {
-  static constexpr int kN = D / 32;
-  int row[kN];        // of the tile
-  uint32_t piece[kN];  // byte offset in it
+  static constexpr int kN = D / 32, kKept = D == 96 ? kN : 1;
+  int row[kKept];        // of the tile
+  uint32_t piece[kKept];  // byte offset in it
   uint32_t wave_at;
   __device__ __forceinline__ RowFetch() {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
+    for (int i = 0; i < kKept; ++i) {
       const int at = i * 256 + threadIdx.x;
       row[i] = at / (D / 8);
       piece[i] = 16 * ((at % (D / 8)) ^ swizzle<D>(row[i]));
     }
     wave_at = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 1024;
   }
-  // Rows of `stride` bytes from `base` (the tile's first row) into `tile`; rows
-  // beyond `last` repeat it.
-  __device__ __forceinline__ void rows(uint64_t base, uint32_t stride, int last, uint32_t tile) const {
+  // 64 rows of `stride` bytes, `from` of those at `base` on, into `tile`; rows
+  // beyond the `last` of them repeat it. Where the rows' pieces are a power of two, a thread's
+  // rows are 2048 / D apart and swizzle alike.
+  __device__ __forceinline__ void rows(uint64_t base, uint32_t stride, int from, int last, uint32_t tile) const {
 #pragma unroll
-    for (int i = 0; i < kN; ++i)
-      fetch_to_lds(base, (uint32_t)min(row[i], last) * stride + piece[i], tile + wave_at + 4096 * i);
+    for (int i = 0; i < kN; ++i) {
+      const int r = kKept == 1 ? row[0] + 2048 / D * i : row[i];
+      fetch_to_lds(base, (uint32_t)min(r + from, last) * stride + piece[kKept == 1 ? 0 : i], tile + wave_at + 4096 * i);
+    }
   }
 };
 
@@ -110,6 +140,14 @@ __device__ __forceinline__ SeqTile seq_tile(const HistoryArgs& a, int tile, int 
   t.r0 = (tile - (t.b + t.first / R)) * R;
   if (t.r0 < 0) t.r0 = t.len;
   return t;
+}
+// Heads and tiles of a grid of heads * tiles blocks, heads fastest. Blocks are
+// dealt to the 8 XCDs in turn; where the heads can be, they are dealt so that an
+// XCD has neighbouring ones, which share their key head, and with it the L2.
+__device__ __forceinline__ void head_and_tile(int block, int heads, FastDiv by_heads, int* head, int* tile) {
+  *tile = div_by(by_heads, block);
+  const int h = block - *tile * heads;
+  *head = heads % 8 == 0 ? (h & 7) * (heads >> 3) + (h >> 3) : h;
 }
 inline long long seq_tiles(long long tokens, int seqs, int R) { return seqs + tokens / R; }
 
@@ -178,59 +216,103 @@ __device__ __forceinline__ Biases biases_of(const HistoryView& h, const BiasLds&
 }
 
 // ---- values that are not numbers ----------------------------------------------
-// Whether any of the wave's 32 rows of D elements at v holds an infinity or NaN.
-template <int DT, int D>
-__device__ __forceinline__ bool any_special(const short* v) {
-  typedef unsigned short us8 __attribute__((ext_vector_type(8)));
-  constexpr unsigned short top = DT == EMB_BF16 ? 0x7f80 : 0x7c00;
-  unsigned m = 0;
-#pragma unroll
-  for (int i = 0; i < 32 * D / 512; ++i) {
-    const us8 x = *reinterpret_cast<const us8*>(v + 8 * (i * 64 + (threadIdx.x & 63)));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m |= (x[j] & top) == top ? 1u : 0u;
+// A product over a tile's rows gives rows that a column does not see a weight of
+// 0, but an infinity or NaN there would still reach it. Only tiles on the diagonal
+// of causal calls and those with the sequence's end have such rows; where one of
+// them holds such values, which is rare, its block takes them out of LDS between
+// the tile's scores, which still need them, and its product, and (for values whose
+// weights are positive) notes where they were: Marks.
+
+constexpr int kNoMark = 0x7fffffff;
+
+// For each of D elements the row nearest to those that do not see it that holds
+// +infinity, -infinity, NaN there: the first (sign 1) or the last (sign -1; all
+// rows times the sign).
+template <int D>
+struct Marks {
+  int at[3][D];
+  __device__ __forceinline__ void clear() {
+    for (int i = threadIdx.x; i < 3 * D; i += blockDim.x) (&at[0][0])[i] = kNoMark;
   }
-  return __ballot(m != 0) != 0;
+};
+
+// Whether the block's `rows` rows of D elements at `tile` hold infinities or NaN.
+// Contains a barrier.
+template <int DT, int D>
+__device__ __forceinline__ bool any_special(const short* tile, int rows) {
+  constexpr uint32_t top = DT == EMB_BF16 ? 0x7f80u : 0x7c00u;
+  int found = 0;
+  for (int i = threadIdx.x; i < rows * (D / 8); i += 256) {
+    const u4 x = *reinterpret_cast<const u4*>(tile + 8 * i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) found |= (x[j] & top) == top || (x[j] >> 16 & top) == top;
+  }
+  return __syncthreads_or(found) != 0;
 }
 
-// acc[d] += (columns of 32 rows of the tile, from row0 on) times w, for a tile in
-// which not every column of w sees every row: those that it does not see have a
-// weight of 0, but an infinity or NaN there would still reach it. Column c sees
-// the rows [lo, hi) (the lane's own), counted from row0. Rare: only tiles with
-// such values come here. One product for each of the bounds, with the rows
-// beyond it cleared, of which each column keeps its own.
+// Takes them out of 32 rows, the first of which is row `first` of `len` of its
+// sequence: rows behind the end become zeros; of the others, where `inside`,
+// infinities and NaN, which go into `marks` (may be null) as rows times `sign`.
 template <int DT, int D>
-__device__ __forceinline__ void guarded_product(f16v (&acc)[D / 32], const short* tile, int row0, const s8v (&w)[2],
-                                                int lo, int hi) {
-#pragma unroll 1
-  for (int a = 0; a < 32; ++a) {
-    // What is worked out from the lane stays in here: held outside, for this rare
-    // path, it would take registers from the common one.
-    int lane = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane));
-    const int l = __builtin_amdgcn_readlane(lo, a), u = __builtin_amdgcn_readlane(hi, a);
-    const bool mine = (lane & 31) == a;
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) {
-      f16v o = acc[d];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        s8v x = column_operand<D>(tile, row0 + 16 * k, d, lane);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int r = 16 * k + 8 * (j / 4) + 4 * (lane >> 5) + j % 4;
-          x[j] = r >= l && r < u ? x[j] : (short)0;
-        }
-        o = mfma<DT>(x, w[k], o);
+__device__ __forceinline__ void clear_special(short* tile, int first, int len, bool inside, Marks<D>* marks, int sign) {
+  constexpr uint32_t top = DT == EMB_BF16 ? 0x7f80u : 0x7c00u;
+  for (int i = threadIdx.x; i < 32 * (D / 8); i += 256) {
+    const int r = i / (D / 8), c = 8 * (i % (D / 8) ^ swizzle<D>(r));
+    short* at = tile + 8 * i;
+    if (first + r >= len) {
+      *reinterpret_cast<s8v*>(at) = s8v{};
+    } else if (inside) {
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t x = (uint16_t)at[j];
+        if ((x & top) != top) continue;
+        at[j] = 0;
+        const int kind = (x & 0x7fffu) > top ? 2 : (int)(x >> 15);
+        if (marks) atomicMin(&marks->at[kind][c + j], sign * (first + r));
       }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) acc[d][i] = mine ? o[i] : acc[d][i];
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
-// Packs the elements of a product, times `by`, for the next one.
+// What the lane's column, at `place` times the sign, sees of the marks, added to
+// its sums.
+template <int D>
+__device__ __forceinline__ void add_marks(f16v (&acc)[D / 32], const Marks<D>& marks, int place) {
+  const int h4 = 4 * ((threadIdx.x & 63) >> 5);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int c = 32 * d + 8 * (i / 4) + h4 + i % 4;
+      const bool u = place >= marks.at[0][c], v = place >= marks.at[1][c], n = place >= marks.at[2][c] || (u && v);
+      acc[d][i] += n ? __builtin_nanf("") : u ? -kNegInf : v ? kNegInf : 0.f;
+    }
+}
+
+// acc[d] += (columns of the 32 rows at `tile`) times w.
+template <int DT, int D>
+__device__ __forceinline__ void add_product(f16v (&acc)[D / 32], const TileLane<D>& at, const short* tile,
+                                            const s8v (&w)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) acc[d] = mfma<DT>(at.columns(tile, 16 * k, d), w[k], acc[d]);
+}
+
+// Which of a product's 32 rows are in [lo, hi): bit 8 (i / 4) + i % 4 for the
+// lane's element i. One register for all of them, where comparisons would hold
+// a mask each.
+__device__ __forceinline__ uint32_t row_bits(int lo, int hi) {
+  const int l = min(max(lo, 0), 32), u = min(max(hi, 0), 32);
+  const uint64_t bits = ((1ull << u) - 1) & ~((1ull << l) - 1);
+  return (uint32_t)bits >> 4 * ((threadIdx.x & 63) >> 5);
+}
+// x where element i's bit is set, else 0 (whatever x is).
+__device__ __forceinline__ float where_bit(uint32_t bits, int i, float x) {
+  const int mask = (int)(bits << (31 - (8 * (i / 4) + i % 4))) >> 31;
+  return __uint_as_float(__float_as_uint(x) & (uint32_t)mask);
+}
+
+// Packs the elements of a product for the next one.
 template <int DT>
 __device__ __forceinline__ void pack_tile(const f16v& x, s8v (&w)[2]) {
 #pragma unroll

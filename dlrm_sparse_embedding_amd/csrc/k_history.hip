@@ -36,17 +36,18 @@ struct Wave {
   float mx, sum;  // running maximum (log2 units) and the lane's part of the sum
 };
 
-// 32 keys. EDGE: not every row sees all of them.
+// Probabilities of 32 keys, packed. EDGE: not every row sees all of them.
 template <int DT, int D, bool BIAS, bool EDGE>
-__device__ __forceinline__ void half_step(const HistoryArgs& a, float scale2, Wave<DT, D>& w, const BiasLds& sb,
-                                          float* win, const short* ks, const short* vs, int k0, int q0, int seen) {
+__device__ __forceinline__ void weights_of(const HistoryArgs& a, float scale2, Wave<DT, D>& w, const BiasLds& sb,
+                                           float* win, const TileLane<D>& tl, const short* ks, int k0, int q0, int seen,
+                                           s8v (&p)[2]) {
   const int lane = threadIdx.x & 63;
   Biases b{};
   if (BIAS) b = biases_of(a.h, sb, q0 + 31 - k0, win);
   f16v s[1];
   s[0] = f16v{};
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(row_operand<D>(ks, 0, i), w.q[i], s[0]);
+  for (int i = 0; i < D / 16; ++i) s[0] = mfma<DT>(tl.rows(ks, 0, i), w.q[i], s[0]);
   float mul = scale2, add = 0.f;  // a score is s * mul + add
   if (BIAS && b.far) add = b.value;
   if (BIAS && !b.far) {
@@ -75,31 +76,20 @@ __device__ __forceinline__ void half_step(const HistoryArgs& a, float scale2, Wa
     sum += s[0][i];
   }
   w.sum += sum;
-  s8v p[2];
   pack_tile<DT>(s[0], p);
-  if (EDGE && any_special<DT, D>(vs)) {
-    guarded_product<DT, D>(w.o, vs, 0, p, 0, seen - k0);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int d = 0; d < D / 32; ++d) w.o[d] = mfma<DT>(column_operand<D>(vs, 16 * k, d), p[k], w.o[d]);
-  }
 }
 
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, FastDiv by_m) {
+__global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, FastDiv by_heads, FastDiv by_m) {
   __shared__ __attribute__((aligned(1024))) short s_k[2][kTile * D], s_v[2][kTile * D];
   __shared__ BiasLds s_bias;
   __shared__ float s_win[BIAS ? 4 : 1][64];
+  __shared__ Marks<D> s_marks;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   report_offsets(a.offsets, a.seqs, a.tokens, a.h.error);
-  // blocks are dealt to the 8 XCDs in turn: those of one head, which read the
-  // same keys, go to one XCD and its L2, later tiles (which see more) first
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int head = id / tiles;
-  if (head >= a.h.q_heads) return;
-  const SeqTile t = seq_tile(a, tiles - 1 - id % tiles, kRows);
+  int head, tile;
+  head_and_tile(blockIdx.x, a.h.q_heads, by_heads, &head, &tile);
+  const SeqTile t = seq_tile(a, tiles - 1 - tile, kRows);  // later tiles, which see more, first
   if (t.r0 >= t.len) return;
   const int kh = div_by(by_m, head);
   const int end = a.h.causal ? min(t.r0 + kRows, t.len) : t.len;
@@ -109,14 +99,15 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
   const uint32_t lds_k = (uint32_t)(uintptr_t)(lds_elem*)&s_k[0][0], lds_v = (uint32_t)(uintptr_t)(lds_elem*)&s_v[0][0];
   const RowFetch<D> f;
   auto fetch = [&](int k0, int b) {
-    f.rows(k_at + (uint64_t)k0 * k_step, k_step, t.len - 1 - k0, lds_k + b * kTile * D * 2);
-    f.rows(v_at + (uint64_t)k0 * v_step, v_step, t.len - 1 - k0, lds_v + b * kTile * D * 2);
+    f.rows(k_at + (uint64_t)k0 * k_step, k_step, 0, t.len - 1 - k0, lds_k + b * kTile * D * 2);
+    f.rows(v_at + (uint64_t)k0 * v_step, v_step, 0, t.len - 1 - k0, lds_v + b * kTile * D * 2);
   };
   fetch(0, 0);
   if (BIAS) {
     stage_bounds(a.h, s_bias);
     stage_bias(a, head, s_bias);
   }
+  s_marks.clear();
   const int q0 = t.r0 + 32 * wave, place = q0 + (lane & 31);
   const bool live = q0 < t.len;
   const long long token = t.first + min(place, t.len - 1);
@@ -128,20 +119,34 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
   w.sum = 0.f;
   const int seen = a.h.causal ? min(place + 1, t.len) : t.len;
   const int seen_by_all = a.h.causal ? min(q0 + 1, t.len) : t.len;
-  const int seen_by_any = a.h.causal ? min(q0 + 32, t.len) : t.len;
+  const int seen_by_any = !live ? 0 : a.h.causal ? min(q0 + 32, t.len) : t.len;
   const float scale2 = a.h.scale * kLog2e;
+  const TileLane<D> lanes;
+  bool marked = false;
   for (int k0 = 0, b = 0; k0 < end; k0 += kTile, b ^= 1) {
     fetched();
     __syncthreads();
     if (k0 + kTile < end) fetch(k0 + kTile, b ^ 1);
-    if (!live) continue;
-    float* win = s_win[BIAS ? wave : 0];
-#pragma unroll
+    const bool diagonal = a.h.causal && k0 >= t.r0;
+    bool special = false;
+    if (diagonal || k0 + kTile > t.len) special = any_special<DT, D>(s_v[b], kTile);
+    marked |= special;
+#pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       const int k = k0 + 32 * n;
-      const short *ks = s_k[b] + 32 * n * D, *vs = s_v[b] + 32 * n * D;
-      if (k + 32 <= seen_by_all) half_step<DT, D, BIAS, false>(a, scale2, w, s_bias, win, ks, vs, k, q0, seen);
-      else if (k < seen_by_any) half_step<DT, D, BIAS, true>(a, scale2, w, s_bias, win, ks, vs, k, q0, seen);
+      short* vs = s_v[b] + 32 * n * D;
+      const TileLane<D> tl = lanes.fresh();
+      s8v p[2];
+      float* win = s_win[BIAS ? wave : 0];
+      if (__builtin_expect(k + 32 <= seen_by_all, 1))
+        weights_of<DT, D, BIAS, false>(a, scale2, w, s_bias, win, tl, s_k[b] + 32 * n * D, k, q0, seen, p);
+      else if (k < seen_by_any)
+        weights_of<DT, D, BIAS, true>(a, scale2, w, s_bias, win, tl, s_k[b] + 32 * n * D, k, q0, seen, p);
+      if (__builtin_expect(special, 0)) {
+        clear_special<DT, D>(vs, k, t.len, diagonal, &s_marks, 1);
+        __syncthreads();
+      }
+      if (k < seen_by_any) add_product<DT, D>(w.o, tl, vs, p);
     }
   }
   if (!live) return;
@@ -155,6 +160,7 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) w.o[d] = f16v{};
   }
+  if (__builtin_expect(marked, 0)) add_marks<D>(w.o, s_marks, place);
   short* dst = reinterpret_cast<short*>(const_cast<void*>(a.out.p)) + token * a.out.ts + head * a.out.hs + 8 * (lane >> 5);
   store_columns<DT, D>(dst, w.o, inv, store);
 }
@@ -162,10 +168,11 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
 template <int DT, int D>
 hipError_t launch(const HistoryArgs& a, hipStream_t st) {
   const long long tiles = seq_tiles(a.tokens, a.seqs, kRows);
-  const unsigned blocks = (unsigned)((tiles * a.h.q_heads + 7) / 8 * 8);
+  const unsigned blocks = (unsigned)(tiles * a.h.q_heads);
+  const FastDiv by_heads = fast_div((uint32_t)a.h.q_heads);
   const FastDiv by_m = fast_div((uint32_t)(a.h.q_heads / a.h.kv_heads));
-  if (a.bias) k_history<DT, D, true><<<blocks, 256, 0, st>>>(a, (int)tiles, by_m);
-  else k_history<DT, D, false><<<blocks, 256, 0, st>>>(a, (int)tiles, by_m);
+  if (a.bias) k_history<DT, D, true><<<blocks, 256, 0, st>>>(a, (int)tiles, by_heads, by_m);
+  else k_history<DT, D, false><<<blocks, 256, 0, st>>>(a, (int)tiles, by_heads, by_m);
   return hipGetLastError();
 }
 

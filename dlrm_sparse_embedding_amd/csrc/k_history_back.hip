@@ -11,9 +11,10 @@
 // The rows' sums. sum_j P_ij dP_ij is dout_i . out_i but for the rounding of out,
 // which is enough for 16-bit results but not for dbias: its fp32 sums cancel (dS
 // sums to zero along each row), and the rounding does not. The first kernel
-// therefore starts from dout . out, sums its own dS along the row, which gives
-// what the start was off by, and hands the corrected sum to the second one, at no
-// further product.
+// therefore starts from dout . out, sums its own dS along the row, which gives e,
+// what the start was off by, hands the corrected sum to the second one, and takes
+// e sum_j P_ij k_j, one product more, off dq (bf16 heads of 64: dq's error against
+// 64 bits 2.5e-3 without it, where rounding the result alone makes 1.7e-3).
 //
 // Precision. P and dS are fp32 and rounded to the heads' type for the products.
 // fp16 ones are scaled first: P by 2^15, dS by a power of two that each column of
@@ -27,13 +28,14 @@ namespace emb {
 
 namespace {
 
-constexpr int kRows = 128;  // rows of a block
+constexpr int kRows = 128;  // queries of a block for dq, and of a tile for dk and dv
+constexpr int kKeys = 64;   // keys of a block for dk and dv
 
 struct BackDev {
   HistoryBackArgs a;
   float scale2;
-  FastDiv by_m;
-  int m, tiles, bias_rows;
+  FastDiv by_m, by_heads, by_kv_heads;
+  int m, q_tiles, k_tiles, bias_rows;
 };
 
 // A power of two for a lane's column of dS and of the sums that it enters.
@@ -71,19 +73,6 @@ struct ColumnScale {
   }
 };
 
-// acc[d] += (columns of 32 rows of `tile`) times w. GUARD: see guarded_product.
-template <int DT, int D, bool GUARD>
-__device__ __forceinline__ void add_product(f16v (&acc)[D / 32], const short* tile, const s8v (&w)[2], int lo, int hi) {
-  if (GUARD && any_special<DT, D>(tile)) {
-    guarded_product<DT, D>(acc, tile, 0, w, lo, hi);
-    return;
-  }
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] = mfma<DT>(column_operand<D>(tile, 16 * k, d), w[k], acc[d]);
-}
-
 // z of a row in log2 units, so that P = 2^(s - z); +infinity for one that sees nothing.
 __device__ __forceinline__ float z_of(float lse) { return lse == kNegInf ? -kNegInf : lse * kLog2e; }
 
@@ -93,22 +82,38 @@ template <int DT, int D>
 struct QueryWave {
   s8v q[D / 16], go[D / 16];
   f16v dq[D / 32];
+  f16v pk[D / 32];  // sum P k (fp16: times 2^15)
   ColumnScale<DT> c;
-  float z, delta, error;  // the row's z, sum of P dP, and this lane's part of what it is off by
+  float z, delta, error;  // the row's z, dout . out, and this lane's part of what that is off by
 };
 
-// 32 keys. EDGE: not every row sees all of them.
+// P packed for a product; fp16 times 2^15 (P is at most 1 but for rounding).
+template <int DT>
+__device__ __forceinline__ void pack_weights(const f16v& p, s8v (&x)[2]) {
+  if constexpr (DT == EMB_F16) {
+    f16v y;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y[i] = p[i] * 0x1p15f;
+    pack_tile<DT>(y, x);
+  } else {
+    pack_tile<DT>(p, x);
+  }
+}
+
+// P and dS of 32 keys, packed. EDGE: not every row sees all of them.
 template <int DT, int D, bool BIAS, bool EDGE>
-__device__ __forceinline__ void dq_step(const BackDev& p, QueryWave<DT, D>& w, const BiasLds& sb, float* win,
-                                        const short* ks, const short* vs, int k0, int q0, int seen) {
+__device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w, const BiasLds& sb, float* win,
+                                           const TileLane<D>& tl, const short* ks, const short* vs, int k0, int q0,
+                                           int seen, s8v (&xp)[2], s8v (&xs)[2]) {
   const int lane = threadIdx.x & 63;
   Biases b{};
   if (BIAS) b = biases_of(p.a.f.h, sb, q0 + 31 - k0, win);
   f16v s{}, dp{};
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) s = mfma<DT>(row_operand<D>(ks, 0, i), w.q[i], s);
+  for (int i = 0; i < D / 16; ++i) s = mfma<DT>(tl.rows(ks, 0, i), w.q[i], s);
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(row_operand<D>(vs, 0, i), w.go[i], dp);
+  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(tl.rows(vs, 0, i), w.go[i], dp);
+  const uint32_t bits = EDGE ? row_bits(0, seen - k0) : 0;
   if (BIAS && !b.far) {
     const float* at = win + 4 * (lane >> 5) + 31 - (lane & 31);
 #pragma unroll
@@ -121,29 +126,29 @@ __device__ __forceinline__ void dq_step(const BackDev& p, QueryWave<DT, D>& w, c
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(s[i]) * (dp[i] - w.delta);
-    if (EDGE && k0 + 8 * (i / 4) + 4 * (lane >> 5) + i % 4 >= seen) s[i] = 0.f;
-    sum += s[i];
+    s[i] = __builtin_amdgcn_exp2f(s[i]);
+    if (EDGE) s[i] = where_bit(bits, i, s[i]);
+    dp[i] = s[i] * (dp[i] - w.delta);
+    if (EDGE) dp[i] = where_bit(bits, i, dp[i]);
+    sum += dp[i];
   }
   w.error += sum;
-  w.c.fit(s, w.dq);
-  s8v ds[2];
-  pack_tile<DT>(w.c.scaled(s), ds);
-  add_product<DT, D, EDGE>(w.dq, ks, ds, 0, seen - k0);
+  w.c.fit(dp, w.dq);
+  pack_weights<DT>(s, xp);
+  pack_tile<DT>(w.c.scaled(dp), xs);
 }
 
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
+__global__ __launch_bounds__(256, D == 128 ? 1 : 2) void k_history_dq(BackDev p) {
   __shared__ __attribute__((aligned(1024))) short s_k[2][kTile * D], s_v[2][kTile * D];
   __shared__ BiasLds s_bias;
   __shared__ float s_win[BIAS ? 4 : 1][64];
   const HistoryArgs& a = p.a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   report_offsets(a.offsets, a.seqs, a.tokens, a.h.error);
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int head = id / p.tiles;
-  if (head >= a.h.q_heads) return;
-  const SeqTile t = seq_tile(a, p.tiles - 1 - id % p.tiles, kRows);
+  int head, tile;
+  head_and_tile(blockIdx.x, a.h.q_heads, p.by_heads, &head, &tile);
+  const SeqTile t = seq_tile(a, p.q_tiles - 1 - tile, kRows);  // later tiles, which see more, first
   if (t.r0 >= t.len) return;
   const int kh = div_by(p.by_m, head);
   const int end = a.h.causal ? min(t.r0 + kRows, t.len) : t.len;
@@ -153,8 +158,8 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
   const uint32_t lds_k = (uint32_t)(uintptr_t)(lds_elem*)&s_k[0][0], lds_v = (uint32_t)(uintptr_t)(lds_elem*)&s_v[0][0];
   const RowFetch<D> f;
   auto fetch = [&](int k0, int b) {
-    f.rows(k_at + (uint64_t)k0 * k_step, k_step, t.len - 1 - k0, lds_k + b * kTile * D * 2);
-    f.rows(v_at + (uint64_t)k0 * v_step, v_step, t.len - 1 - k0, lds_v + b * kTile * D * 2);
+    f.rows(k_at + (uint64_t)k0 * k_step, k_step, 0, t.len - 1 - k0, lds_k + b * kTile * D * 2);
+    f.rows(v_at + (uint64_t)k0 * v_step, v_step, 0, t.len - 1 - k0, lds_v + b * kTile * D * 2);
   };
   fetch(0, 0);
   if (BIAS) {
@@ -184,31 +189,62 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
   w.z = z_of(a.lse[token * a.h.q_heads + head]);
   w.error = 0.f;
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d) w.dq[d] = f16v{};
+  for (int d = 0; d < D / 32; ++d) w.dq[d] = w.pk[d] = f16v{};
+  const TileLane<D> lanes;
   const int seen = a.h.causal ? min(place + 1, t.len) : t.len;
   const int seen_by_all = a.h.causal ? min(q0 + 1, t.len) : t.len;
-  const int seen_by_any = a.h.causal ? min(q0 + 32, t.len) : t.len;
+  const int seen_by_any = !live ? 0 : a.h.causal ? min(q0 + 32, t.len) : t.len;
   for (int k0 = 0, b = 0; k0 < end; k0 += kTile, b ^= 1) {
     fetched();
     __syncthreads();
     if (k0 + kTile < end) fetch(k0 + kTile, b ^ 1);
-    if (!live) continue;
-    float* win = s_win[BIAS ? wave : 0];
-#pragma unroll
+    const bool diagonal = a.h.causal && k0 >= t.r0;
+    bool special = false;
+    if (diagonal || k0 + kTile > t.len) special = any_special<DT, D>(s_k[b], kTile);
+#pragma unroll 1
     for (int n = 0; n < 2; ++n) {
       const int k = k0 + 32 * n;
-      const short *ks = s_k[b] + 32 * n * D, *vs = s_v[b] + 32 * n * D;
-      if (k + 32 <= seen_by_all) dq_step<DT, D, BIAS, false>(p, w, s_bias, win, ks, vs, k, q0, seen);
-      else if (k < seen_by_any) dq_step<DT, D, BIAS, true>(p, w, s_bias, win, ks, vs, k, q0, seen);
+      short* ks = s_k[b] + 32 * n * D;
+      const short* vs = s_v[b] + 32 * n * D;
+      const TileLane<D> tl = lanes.fresh();
+      s8v xp[2], xs[2];
+      float* win = s_win[BIAS ? wave : 0];
+      if (__builtin_expect(k + 32 <= seen_by_all, 1))
+        dq_weights<DT, D, BIAS, false>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, xp, xs);
+      else if (k < seen_by_any)
+        dq_weights<DT, D, BIAS, true>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, xp, xs);
+      if (__builtin_expect(special, 0)) {
+        __syncthreads();
+        clear_special<DT, D>(ks, k, t.len, diagonal, nullptr, 0);
+        __syncthreads();
+      }
+      if (k >= seen_by_any) continue;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          const s8v x = tl.columns(ks, 16 * kk, d);
+          w.dq[d] = mfma<DT>(x, xs[kk], w.dq[d]);
+          w.pk[d] = mfma<DT>(x, xp[kk], w.pk[d]);
+        }
     }
   }
   if (!live) return;
   const bool store = place < t.len;
-  const float delta = w.delta + both_halves_sum(w.error);
-  if (store && lane < 32) p.a.rows[(long long)head * a.tokens + token] = delta;
+  const float error = both_halves_sum(w.error);
+  if (store && lane < 32) {
+    p.a.rows[(long long)head * a.tokens + token] = w.delta + error;
+    p.a.rows[(long long)(a.h.q_heads + head) * a.tokens + token] = w.z;
+  }
+  // dS is off by error * P, and dq by error * sum P k
+  const float by = 1.f / w.c.c, off = error * (DT == EMB_F16 ? 0x1p-15f : 1.f);
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w.dq[d][i] = w.dq[d][i] * by - off * w.pk[d][i];
   short* dst = reinterpret_cast<short*>(const_cast<void*>(p.a.dq.p)) + token * p.a.dq.ts + head * p.a.dq.hs +
                8 * (lane >> 5);
-  store_columns<DT, D>(dst, w.dq, a.h.scale / w.c.c, store);
+  store_columns<DT, D>(dst, w.dq, a.h.scale, store);
 }
 
 // ---- dk, dv and dbias -----------------------------------------------------------
@@ -220,62 +256,76 @@ struct KeyWave {
   ColumnScale<DT> c;
 };
 
-constexpr int kDiag = 40;  // stride of dS in LDS: the lanes' halves, 4 rows apart, lie in different banks
-
-// What the second kernel keeps in LDS for the bias' gradient, a part for each wave.
+// The second kernel's sums of the bias' gradient, a part for each wave.
 template <bool BIAS>
 struct GradLds {
-  float ds[4][32 + 32 * kDiag + 32];
   float sum[4][2 * EMB_MAX_BUCKETS];
 };
 template <>
 struct GradLds<false> {};
 
-// Adds a tile's dS to the sums of its rows of the bias: along its 63 diagonals, a
-// lane for each, then over the neighbouring lanes of one row, in a fixed order.
-__device__ __forceinline__ void add_diagonals(const f16v& s, int row, float* ds, float* sum) {
-  const int lane = threadIdx.x & 63, c = lane & 31;
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+// One step of a running sum over the neighbouring lanes of one row: adds what the
+// lane that CTRL names has, if its row is the same.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float same_row(float v, int row) {
+  const float x = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+  const int r = __builtin_amdgcn_update_dpp(-2, row, CTRL, ROWS, 0xf, false);
+  return v + (r == row ? x : 0.f);
+}
+
+// Adds a tile's dS to the sums of its rows of the bias, in a fixed order: along
+// its 63 diagonals, by turning row r's lanes r places, then over the neighbouring
+// diagonals of one row of the bias. `row`: of diagonal `lane`, 31 - r + c of (r, c).
+__device__ __forceinline__ void add_diagonals(const f16v& s, int row, float* sum) {
+  const int lane = threadIdx.x & 63, l = (lane & 31) + 4 * (lane >> 5);
+  // what comes to lane l of 32 from place l + r is of diagonal 31 + l, or, from
+  // behind the end, of diagonal l - 1
+  float upper = 0.f, lower = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) ds[32 + (8 * (i / 4) + 4 * (lane >> 5) + i % 4) * kDiag + c] = s[i];
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  // diagonal x holds (r, c) with 31 - r + c = x
-  float v = 0.f;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r) {
-    const int at = lane - 31 + r;
-    const float x = ds[32 + r * kDiag + min(max(at, 0), 31)];
-    v += at >= 0 && at < 32 ? x : 0.f;
+  for (int i = 0; i < 16; ++i) {
+    const int from = l + 8 * (i / 4) + i % 4;
+    const float x = __int_as_float(__builtin_amdgcn_ds_bpermute(4 * ((from & 31) | (lane & 32)), __float_as_int(s[i])));
+    const bool wraps = from >= 32;
+    upper += wraps ? 0.f : x;
+    lower += wraps ? x : 0.f;
   }
-  if (lane == 63) row = -1;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const float x = __shfl_down(v, d, 64);
-    const int r = __shfl_down(row, d, 64);
-    if (lane + d < 64 && r == row) v += x;
+  upper = both_halves_sum(upper);
+  lower = both_halves_sum(lower);
+  const float u = __shfl(upper, (lane + 1) & 31, 64), w = __shfl(lower, (lane + 1) & 31, 64);  // lanes 31 .. 62, 0 .. 30
+  float v = lane < 31 ? w : u;
+  if (lane == 63) {
+    row = -1;
+    v = 0.f;
   }
-  const int before = __shfl_up(row, 1, 64);
-  if (row >= 0 && (lane == 0 || before != row)) sum[row] += v;
+  v = same_row<0x111, 0xf>(v, row);  // one lane up, then two, four and eight inside rows of 16
+  v = same_row<0x112, 0xf>(v, row);
+  v = same_row<0x114, 0xf>(v, row);
+  v = same_row<0x118, 0xf>(v, row);
+  v = same_row<0x142, 0xa>(v, row);  // lane 15 of the row below
+  v = same_row<0x143, 0xc>(v, row);  // lane 31
+  const int next = __shfl_down(row, 1, 64);
+  if (row >= 0 && next != row) sum[row] += v;
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// 32 queries from q0 on. EDGE: not every key is seen by all of them.
-template <int DT, int D, bool BIAS, bool EDGE>
-__device__ __forceinline__ void dkv_step(const BackDev& p, KeyWave<DT, D>& w, const BiasLds& sb, float* win,
-                                         GradLds<BIAS>& g, float (&far)[2], const short* qs, const short* gs,
-                                         const float* zs, const float* deltas, int q0, int k0, int len) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h4 = 4 * (lane >> 5);
-  Biases b{};
-  if (BIAS) b = biases_of(p.a.f.h, sb, q0 + 31 - k0, win);
-  f16v s{}, dp{};
+// Scores' products of 32 queries (rows) and the wave's keys.
+template <int DT, int D>
+__device__ __forceinline__ void dkv_products(const KeyWave<DT, D>& w, const TileLane<D>& tl, const short* qs,
+                                             const short* gs, f16v& s, f16v& dp) {
+  s = f16v{};
+  dp = f16v{};
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) s = mfma<DT>(row_operand<D>(qs, 0, i), w.k[i], s);
+  for (int i = 0; i < D / 16; ++i) s = mfma<DT>(tl.rows(qs, 0, i), w.k[i], s);
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(row_operand<D>(gs, 0, i), w.v[i], dp);
-  const int key = k0 + (lane & 31);
-  // the rows that see the key; none sees one behind the end
-  const int first = p.a.f.h.causal ? key - q0 : 0, end = key < len ? len - q0 : 0;
+  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(tl.rows(gs, 0, i), w.v[i], dp);
+}
+
+// From the products to P (packed, scaled) and dS. bits: the rows that see the
+// lane's key, used where EDGE.
+template <int DT, bool BIAS, bool EDGE>
+__device__ __forceinline__ void dkv_weights(float scale2, const Biases& b, const float* win, const float* zs,
+                                            const float* deltas, uint32_t bits, f16v& s, const f16v& dp, s8v (&x)[2]) {
+  const int lane = threadIdx.x & 63, h4 = 4 * (lane >> 5);
   // diagonal of (r, c): 31 - r + c
   const float* at = win + 31 - h4 + (lane & 31);
 #pragma unroll
@@ -284,47 +334,59 @@ __device__ __forceinline__ void dkv_step(const BackDev& p, KeyWave<DT, D>& w, co
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float add = !BIAS ? 0.f : b.far ? b.value : at[-(2 * i4 + j)];
-      float e = __builtin_amdgcn_exp2f(fmaf(s[i4 + j], p.scale2, add - z[j]));
-      if (EDGE) e = 2 * i4 + h4 + j >= first && 2 * i4 + h4 + j < end ? e : 0.f;
-      s[i4 + j] = e;
+      float e = __builtin_amdgcn_exp2f(fmaf(s[i4 + j], scale2, add - z[j]));
+      s[i4 + j] = EDGE ? where_bit(bits, i4 + j, e) : e;
     }
   }
-  s8v x[2];
-  if constexpr (DT == EMB_F16) {
-    f16v y;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) y[i] = s[i] * 0x1p15f;
-    pack_tile<DT>(y, x);
-  } else {
-    pack_tile<DT>(s, x);
-  }
-  add_product<DT, D, EDGE>(w.dv, gs, x, first, end);
+  pack_weights<DT>(s, x);
 #pragma unroll
   for (int i4 = 0; i4 < 16; i4 += 4) {
     const f4 delta = *reinterpret_cast<const f4*>(deltas + 2 * i4 + h4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float e = s[i4 + j] * (dp[i4 + j] - delta[j]);
-      if (EDGE) e = 2 * i4 + h4 + j >= first && 2 * i4 + h4 + j < end ? e : 0.f;
-      s[i4 + j] = e;
+      s[i4 + j] = EDGE ? where_bit(bits, i4 + j, e) : e;
     }
   }
+}
+
+// A tile's dS into the sums of the bias' gradient.
+template <bool BIAS>
+__device__ __forceinline__ void add_dbias(const BackDev& p, const Biases& b, const f16v& s, GradLds<BIAS>& g,
+                                          float (&far)[2]) {
   if constexpr (BIAS) {
-    if (p.a.dbias) {
-      if (b.far) {
-        float sum = 0.f;
+    if (!p.a.dbias) return;
+    if (b.far) {
+      float sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sum += s[i];
-        if (b.row < p.a.f.h.buckets.n) far[0] += sum;
-        else far[1] += sum;
-      } else {
-        add_diagonals(s, b.row, g.ds[wave], g.sum[wave]);
-      }
+      for (int i = 0; i < 16; ++i) sum += s[i];
+      if (b.row < p.a.f.h.buckets.n) far[0] += sum;
+      else far[1] += sum;
+    } else {
+      const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+      add_diagonals(s, b.row, g.sum[wave]);
     }
   }
+}
+
+// P and dS of 32 queries from q0 on, packed. EDGE: not every key is seen by all of
+// them.
+template <int DT, int D, bool BIAS, bool EDGE>
+__device__ __forceinline__ void dkv_step(const BackDev& p, KeyWave<DT, D>& w, const BiasLds& sb, float* win,
+                                         GradLds<BIAS>& g, float (&far)[2], const TileLane<D>& tl, const short* qs,
+                                         const short* gs, const float* zs, const float* deltas, int q0, int k0, int len,
+                                         s8v (&xp)[2], s8v (&xs)[2]) {
+  Biases b{};
+  if (BIAS) b = biases_of(p.a.f.h, sb, q0 + 31 - k0, win);
+  const int key = k0 + (threadIdx.x & 31);
+  // the rows that see the key; none sees one behind the end
+  const uint32_t bits = EDGE ? row_bits(p.a.f.h.causal ? key - q0 : 0, key < len ? len - q0 : 0) : 0;
+  f16v s, dp;
+  dkv_products<DT, D>(w, tl, qs, gs, s, dp);
+  dkv_weights<DT, BIAS, EDGE>(p.scale2, b, win, zs, deltas, bits, s, dp, xp);
+  add_dbias<BIAS>(p, b, s, g, far);
   w.c.fit(s, w.dk);
-  pack_tile<DT>(w.c.scaled(s), x);
-  add_product<DT, D, EDGE>(w.dk, qs, x, first, end);
+  pack_tile<DT>(w.c.scaled(s), xs);
 }
 
 __device__ __forceinline__ float wave_sum(float x) {
@@ -333,19 +395,24 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
+// A block takes 64 keys of one key head and goes along the query tiles of 128 rows
+// of each of its query heads; waves 0 and 1 take the tiles' first 64 rows for 32
+// keys each, waves 2 and 3 the last 64, and are added to them at the end. So there
+// are twice as many blocks, half as long, as with 128 keys.
 template <int DT, int D, bool BIAS>
 __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p) {
-  __shared__ __attribute__((aligned(1024))) short s_q[2][kTile * D], s_g[2][kTile * D];
-  __shared__ __attribute__((aligned(16))) float s_z[2][kTile], s_delta[2][kTile];
+  constexpr int kPart = kRows * D;  // elements of a tile
+  __shared__ __attribute__((aligned(1024))) short s_tiles[4 * kPart];  // queries twice, dout twice
+  __shared__ __attribute__((aligned(16))) float s_z[2][kRows], s_delta[2][kRows];
   __shared__ BiasLds s_bias;
   __shared__ GradLds<BIAS> s_grad;
   __shared__ float s_win[BIAS ? 4 : 1][64];
+  __shared__ Marks<D> s_marks;
   const HistoryArgs& a = p.a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int id = xcd_remap(blockIdx.x, gridDim.x);
-  const int kh = id / p.tiles, tile = id % p.tiles;
-  if (kh >= a.h.kv_heads) return;
-  const SeqTile t = seq_tile(a, tile, kRows);
+  int kh, tile;
+  head_and_tile(blockIdx.x, a.h.kv_heads, p.by_kv_heads, &kh, &tile);
+  const SeqTile t = seq_tile(a, tile, kKeys);
   const bool grad = BIAS && p.a.dbias;
   float* part = p.a.part + ((long long)tile * a.h.q_heads + kh * p.m) * p.bias_rows;
   if (t.r0 >= t.len) {
@@ -353,7 +420,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p)
       for (int i = threadIdx.x; i < p.m * p.bias_rows; i += 256) part[i] = 0.f;
     return;
   }
-  const int k0 = t.r0 + 32 * wave, place = k0 + (lane & 31);
+  const int k0 = t.r0 + 32 * (wave & 1), place = k0 + (lane & 31);
+  const int row0 = 64 * (wave >> 1);  // the wave's rows of a tile
   const bool live = k0 < t.len;
   const long long token = t.first + min(place, t.len - 1);
   KeyWave<DT, D> w;
@@ -361,56 +429,76 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p)
   load_operands<D>(a.v, token, kh, w.v);
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) w.dk[d] = w.dv[d] = f16v{};
-  const int begin = a.h.causal ? t.r0 : 0;
+  const int begin = a.h.causal ? t.r0 / kRows * kRows : 0;
   const uint32_t q_step = 2 * (uint32_t)a.q.ts, g_step = 2 * (uint32_t)p.a.dout.ts;
-  const uint32_t lds_q = (uint32_t)(uintptr_t)(lds_elem*)&s_q[0][0], lds_g = (uint32_t)(uintptr_t)(lds_elem*)&s_g[0][0];
+  const uint32_t lds = (uint32_t)(uintptr_t)(lds_elem*)s_tiles;
+  const uint32_t lds_z = (uint32_t)(uintptr_t)(lds_word*)&s_z[0][0];
+  const uint32_t lds_delta = (uint32_t)(uintptr_t)(lds_word*)&s_delta[0][0];
   const RowFetch<D> f;
+  const TileLane<D> lanes;
+  bool marked = false;
+  s_marks.clear();
   if (BIAS) stage_bounds(a.h, s_bias);
   for (int hh = 0; hh < p.m; ++hh) {
     const int head = kh * p.m + hh;
     const uint64_t q_at = uniform((uint64_t)a.q.p + 2 * (t.first * a.q.ts + head * a.q.hs));
     const uint64_t g_at = uniform((uint64_t)p.a.dout.p + 2 * (t.first * p.a.dout.ts + head * p.a.dout.hs));
+    // the rows' sums and z: waves 0 and 2 fetch the one, 1 and 3 the other
+    const uint64_t word_at = uniform(
+        (uint64_t)(p.a.rows + (long long)((wave & 1 ? a.h.q_heads : 0) + head) * a.tokens + t.first));
     auto fetch = [&](int q0, int b) {
-      f.rows(q_at + (uint64_t)q0 * q_step, q_step, t.len - 1 - q0, lds_q + b * kTile * D * 2);
-      f.rows(g_at + (uint64_t)q0 * g_step, g_step, t.len - 1 - q0, lds_g + b * kTile * D * 2);
-    };
-    // z and the rows' sums of a tile, by a thread each
-    auto row_values = [&](int q0, int b) {
-      if (threadIdx.x < kTile) {
-        const long long at = t.first + min(q0 + (int)threadIdx.x, t.len - 1);
-        s_z[b][threadIdx.x] = z_of(a.lse[at * a.h.q_heads + head]);
-      } else if (threadIdx.x < 2 * kTile) {
-        const long long at = t.first + min(q0 + (int)threadIdx.x - kTile, t.len - 1);
-        s_delta[b][threadIdx.x - kTile] = p.a.rows[(long long)head * a.tokens + at];
+      const int last = t.len - 1 - q0;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        f.rows(q_at + (uint64_t)q0 * q_step, q_step, 64 * n, last, lds + 2 * (b * kPart + n * 64 * D));
+        f.rows(g_at + (uint64_t)q0 * g_step, g_step, 64 * n, last, lds + 2 * ((2 + b) * kPart + n * 64 * D));
       }
+      fetch_word_to_lds(word_at + 4 * (uint64_t)q0, 4 * (uint32_t)min(row0 + lane, last),
+                        (wave & 1 ? lds_z : lds_delta) + 4 * (b * kRows + row0));
     };
     __syncthreads();  // the last head's tiles and bias are done with
     fetch(begin, 0);
-    row_values(begin, 0);
     if (BIAS) stage_bias(a, head, s_bias);
     if constexpr (BIAS) {
       for (int i = threadIdx.x; i < 4 * 2 * EMB_MAX_BUCKETS; i += 256) (&s_grad.sum[0][0])[i] = 0.f;
     }
     float far[2] = {0.f, 0.f};
-    for (int q0 = begin, b = 0; q0 < t.len; q0 += kTile, b ^= 1) {
+    for (int q0 = begin, b = 0; q0 < t.len; q0 += kRows, b ^= 1) {
       fetched();
       __syncthreads();
-      if (q0 + kTile < t.len) {
-        fetch(q0 + kTile, b ^ 1);
-        row_values(q0 + kTile, b ^ 1);
-      }
-      if (!live) continue;
+      if (q0 + kRows < t.len) fetch(q0 + kRows, b ^ 1);
+      short *qs = s_tiles + b * kPart, *gs = s_tiles + (2 + b) * kPart;
+      const bool diagonal = a.h.causal && q0 < t.r0 + kKeys;
+      bool special = false;
+      if (diagonal || q0 + kRows > t.len)
+        special = any_special<DT, D>(qs, kRows) + any_special<DT, D>(gs, kRows) > 0;  // each has its barrier
+      marked |= special;
       float* win = s_win[BIAS ? wave : 0];
-#pragma unroll
+#pragma unroll 1
       for (int n = 0; n < 2; ++n) {
-        const int q = q0 + 32 * n;
-        if (q >= t.len || (a.h.causal && q + 31 < k0)) continue;
-        const short *qs = s_q[b] + 32 * n * D, *gs = s_g[b] + 32 * n * D;
-        const float *zs = s_z[b] + 32 * n, *deltas = s_delta[b] + 32 * n;
-        if (q + 32 <= t.len && (a.h.causal ? q >= k0 + 31 : k0 + 32 <= t.len))
-          dkv_step<DT, D, BIAS, false>(p, w, s_bias, win, s_grad, far, qs, gs, zs, deltas, q, k0, t.len);
-        else
-          dkv_step<DT, D, BIAS, true>(p, w, s_bias, win, s_grad, far, qs, gs, zs, deltas, q, k0, t.len);
+        const int r = row0 + 32 * n, q = q0 + r;
+        const TileLane<D> tl = lanes.fresh();
+        s8v xp[2], xs[2];
+        const bool some = live && q < t.len && !(a.h.causal && q + 31 < k0);
+        const float *zs = s_z[b] + r, *deltas = s_delta[b] + r;
+        if (__builtin_expect(some && q + 32 <= t.len && (a.h.causal ? q >= k0 + 31 : k0 + 32 <= t.len), 1))
+          dkv_step<DT, D, BIAS, false>(p, w, s_bias, win, s_grad, far, tl, qs + r * D, gs + r * D, zs, deltas, q, k0,
+                                       t.len, xp, xs);
+        else if (some)
+          dkv_step<DT, D, BIAS, true>(p, w, s_bias, win, s_grad, far, tl, qs + r * D, gs + r * D, zs, deltas, q, k0,
+                                      t.len, xp, xs);
+        if (__builtin_expect(special, 0)) {
+          __syncthreads();
+          for (int half = 0; half < 2; ++half) {
+            const int at = 64 * half + 32 * n;
+            clear_special<DT, D>(qs + at * D, q0 + at, t.len, diagonal, (Marks<D>*)nullptr, 0);
+            clear_special<DT, D>(gs + at * D, q0 + at, t.len, diagonal, &s_marks, -1);
+          }
+          __syncthreads();
+        }
+        if (!some) continue;
+        add_product<DT, D>(w.dv, tl, gs + r * D, xp);
+        add_product<DT, D>(w.dk, tl, qs + r * D, xs);
       }
     }
     if constexpr (BIAS) {
@@ -427,11 +515,33 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p)
       }
     }
   }
-  if (!live) return;
+  // waves 2 and 3 hand theirs to 0 and 1
+  float* hand = reinterpret_cast<float*>(s_tiles) + (wave & 1) * 64 * D + lane;
+  const float by = 1.f / w.c.c;
+  __syncthreads();
+  if (wave >= 2) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        hand[64 * (16 * d + i)] = w.dk[d][i] * by;
+        hand[64 * (16 * (D / 32 + d) + i)] = w.dv[d][i];
+      }
+  }
+  __syncthreads();
+  if (wave >= 2 || !live) return;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      w.dk[d][i] = w.dk[d][i] * by + hand[64 * (16 * d + i)];
+      w.dv[d][i] += hand[64 * (16 * (D / 32 + d) + i)];
+    }
+  if (__builtin_expect(marked, 0)) add_marks<D>(w.dv, s_marks, -place);
   const bool store = place < t.len;
   short* dk = reinterpret_cast<short*>(const_cast<void*>(p.a.dk.p)) + token * p.a.dk.ts + kh * p.a.dk.hs + 8 * (lane >> 5);
   short* dv = reinterpret_cast<short*>(const_cast<void*>(p.a.dv.p)) + token * p.a.dv.ts + kh * p.a.dv.hs + 8 * (lane >> 5);
-  store_columns<DT, D>(dk, w.dk, a.h.scale / w.c.c, store);
+  store_columns<DT, D>(dk, w.dk, a.h.scale, store);
   store_columns<DT, D>(dv, w.dv, DT == EMB_F16 ? 0x1p-15f : 1.f, store);
 }
 
@@ -453,21 +563,16 @@ __global__ __launch_bounds__(256) void k_history_dbias(const float* __restrict__
 template <int DT, int D, bool BIAS>
 hipError_t launch(const BackDev& p, hipStream_t st) {
   const HistoryView& h = p.a.f.h;
-  const long long tiles = p.tiles;
-  if (p.a.f.tokens == 0) {
-    k_history_dbias<<<(unsigned)(p.bias_rows * h.q_heads), 256, 0, st>>>(nullptr, 0, h.q_heads, p.bias_rows, p.a.dbias);
-    return hipGetLastError();
+  if (p.a.f.tokens > 0) {
+    k_history_dq<DT, D, BIAS><<<(unsigned)(p.q_tiles * h.q_heads), 256, 0, st>>>(p);
+    if (hipError_t e = hipGetLastError()) return e;
+    k_history_dkv<DT, D, BIAS><<<(unsigned)(p.k_tiles * h.kv_heads), 256, 0, st>>>(p);
+    if (hipError_t e = hipGetLastError()) return e;
   }
-  k_history_dq<DT, D, BIAS><<<(unsigned)((tiles * h.q_heads + 7) / 8 * 8), 256, 0, st>>>(p);
-  if (hipError_t e = hipGetLastError()) return e;
-  k_history_dkv<DT, D, BIAS><<<(unsigned)((tiles * h.kv_heads + 7) / 8 * 8), 256, 0, st>>>(p);
-  if (hipError_t e = hipGetLastError()) return e;
-  if (BIAS && p.a.dbias) {
-    k_history_dbias<<<(unsigned)(p.bias_rows * h.q_heads), 256, 0, st>>>(p.a.part, p.tiles, h.q_heads, p.bias_rows,
-                                                                        p.a.dbias);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  if (BIAS && p.a.dbias)
+    k_history_dbias<<<(unsigned)(p.bias_rows * h.q_heads), 256, 0, st>>>(p.a.part, p.a.f.tokens > 0 ? p.k_tiles : 0,
+                                                                        h.q_heads, p.bias_rows, p.a.dbias);
+  return hipGetLastError();
 }
 
 template <int DT>
@@ -485,8 +590,8 @@ hipError_t launch_t(const BackDev& p, hipStream_t st) {
 HistoryBackPlan history_back_plan(const HistoryView& h, long long tokens, int seqs) {
   HistoryBackPlan p{};
   const long long rows = h.buckets.n * (h.causal ? 1 : 2);
-  p.part_off = ((size_t)tokens * h.q_heads * 4 + 255) & ~size_t(255);
-  p.bytes = p.part_off + (size_t)(seq_tiles(tokens, seqs, kRows) * h.q_heads * rows * 4);
+  p.part_off = ((size_t)tokens * h.q_heads * 8 + 255) & ~size_t(255);
+  p.bytes = p.part_off + (size_t)(seq_tiles(tokens, seqs, kKeys) * h.q_heads * rows * 4);
   return p;
 }
 
@@ -496,7 +601,10 @@ hipError_t launch_history_back(const HistoryBackArgs& a, hipStream_t st) {
   p.scale2 = a.f.h.scale * kLog2e;
   p.m = a.f.h.q_heads / a.f.h.kv_heads;
   p.by_m = fast_div((uint32_t)p.m);
-  p.tiles = (int)seq_tiles(a.f.tokens, a.f.seqs, kRows);
+  p.by_heads = fast_div((uint32_t)a.f.h.q_heads);
+  p.by_kv_heads = fast_div((uint32_t)a.f.h.kv_heads);
+  p.q_tiles = (int)seq_tiles(a.f.tokens, a.f.seqs, kRows);
+  p.k_tiles = (int)seq_tiles(a.f.tokens, a.f.seqs, kKeys);
   p.bias_rows = a.f.h.buckets.n * (a.f.h.causal ? 1 : 2);
   return a.f.h.dtype == EMB_BF16 ? launch_t<EMB_BF16>(p, st) : launch_t<EMB_F16>(p, st);
 }

@@ -105,6 +105,7 @@ __global__ __launch_bounds__(256, 2) void k_history_step(StepDev p) {
 #pragma unroll
   for (int d = 0; d < D / 32; ++d) o[d] = f16v{};
   float mx = kNegInf, sum = 0.f;
+  const TileLane<D> tl;
   const int far_from = BIAS ? a.h.buckets.first[a.h.buckets.n - 1] : 0;
 
   for (int k = begin; k < k1; k += 128) {
@@ -163,7 +164,7 @@ __global__ __launch_bounds__(256, 2) void k_history_step(StepDev p) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk)
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) o[d] = mfma<DT>(column_operand<D>(v, 16 * kk, d), w[kk], o[d]);
+      for (int d = 0; d < D / 32; ++d) o[d] = mfma<DT>(tl.columns(v, 16 * kk, d), w[kk], o[d]);
   }
 
   // join: waves 2 and 3 into 0 and 1, then 1 into 0

@@ -213,7 +213,7 @@ struct HistoryBackArgs {
   HistoryArgs f;
   Heads dout, dq, dk, dv;
   float* dbias;  // may be null
-  float* rows;   // workspace: [q_heads][tokens] sums P dP
+  float* rows;   // workspace: [2][q_heads][tokens]: sums P dP, z in log2 units
   float* part;   // workspace: [blocks][rows of the bias] partial sums of dbias
 };
 // What the workspace holds (bytes): the rows' sums, then the partial sums.
