@@ -37,6 +37,11 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE,
           # never emit packed-fp32 VALU ops (v_pk_{add,mul,fma}_f32)
           "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 
+# Options of single sources. k_history_back.hip: its waves use more than 256 registers; products then go to the
+# accumulation registers, from where vector instructions fetch them one by one. In vector form only what does not fit
+# elsewhere stays there.
+EXTRA = {"k_history_back.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+
 
 def _torch_lib_dir() -> str | None:
     try:
@@ -53,7 +58,7 @@ def _torch_lib_dir() -> str | None:
 
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC, *COMMON, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *COMMON, *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd = [HIPCC, "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", CSRC, "-Wall",
                "-x", "hip", f"--offload-arch={ARCH}",

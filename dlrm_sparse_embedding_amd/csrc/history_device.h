@@ -195,11 +195,17 @@ struct Biases {
   int row;      // uniform where far, else the lane's
 };
 // delta_max: the largest distance (query place minus key place).
-__device__ __forceinline__ Biases biases_of(const HistoryView& h, const BiasLds& s, int delta_max, float* win) {
+__device__ __forceinline__ bool all_far(const HistoryView& h, int delta_max, int delta_min) {
+  const int bound = h.buckets.first[h.buckets.n - 1];
+  return delta_min >= bound || (!h.causal && delta_max <= -bound);
+}
+// near: the window also where all are far.
+__device__ __forceinline__ Biases biases_of(const HistoryView& h, const BiasLds& s, int delta_max, float* win,
+                                            bool near = false) {
   Biases b;
   const int last = h.buckets.n - 1, bound = h.buckets.first[last];
   const int delta_min = delta_max - 62;
-  b.far = delta_min >= bound || (!h.causal && delta_max <= -bound);
+  b.far = !near && all_far(h, delta_max, delta_min);
   if (b.far) {
     b.row = delta_min >= bound ? last : last + h.buckets.n;
     b.value = s.value[b.row];
@@ -288,6 +294,52 @@ __device__ __forceinline__ void add_marks(f16v (&acc)[D / 32], const Marks<D>& m
     }
 }
 
+// The operands of 32 rows of a tile, read together ahead of the products that use
+// them: left to the compiler, each product waits for its own read.
+template <int D>
+struct RowOps {
+  s8v x[D / 16];
+  __device__ __forceinline__ void read(const TileLane<D>& at, const short* tile) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) x[i] = at.rows(tile, 0, i);
+  }
+  template <int DT>
+  __device__ __forceinline__ f16v times(const s8v (&w)[D / 16]) const {
+    f16v s{};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) s = mfma<DT>(x[i], w[i], s);
+    return s;
+  }
+};
+template <int D>
+struct ColumnOps {
+  s8v x[2][D / 32];
+  __device__ __forceinline__ void read(const TileLane<D>& at, const short* tile) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) x[k][d] = at.columns(tile, 16 * k, d);
+  }
+  template <int DT>
+  __device__ __forceinline__ void times(f16v (&acc)[D / 32], const s8v (&w)[2]) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int d = 0; d < D / 32; ++d) acc[d] = mfma<DT>(x[k][d], w[k], acc[d]);
+  }
+};
+// Nothing moves across it.
+__device__ __forceinline__ void stage() { __builtin_amdgcn_sched_barrier(0); }
+// Asks for N products with VALU vector instructions behind each of them.
+template <int N, int VALU>
+__device__ __forceinline__ void interleave() {
+  if constexpr (N > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 0);
+    interleave<N - 1, VALU>();
+  }
+}
+
 // acc[d] += (columns of the 32 rows at `tile`) times w.
 template <int DT, int D>
 __device__ __forceinline__ void add_product(f16v (&acc)[D / 32], const TileLane<D>& at, const short* tile,
@@ -341,12 +393,16 @@ __device__ __forceinline__ void store_columns(short* dst, const f16v (&o)[D / 32
     }
 }
 
-// The operands of row `row` (one a lane column) of a heads operand.
+// The operands of a token (one a lane column). They are waited for here: left to
+// their first use, inside the loop over the tiles, the wait would be repeated there
+// and take in the tile that has just been asked for.
 template <int D>
 __device__ __forceinline__ void load_operands(const Heads& x, long long token, int head, s8v (&f)[D / 16]) {
   const short* src = reinterpret_cast<const short*>(x.p) + token * x.ts + head * x.hs + 8 * ((threadIdx.x & 63) >> 5);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) f[i] = *reinterpret_cast<const s8v*>(src + 16 * i);
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) asm volatile("" : "+v"(f[i]));
 }
 
 }  // namespace emb

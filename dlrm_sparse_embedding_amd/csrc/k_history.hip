@@ -36,10 +36,10 @@ struct Wave {
   float mx, sum;  // running maximum (log2 units) and the lane's part of the sum
 };
 
-// Probabilities of 32 keys, packed. EDGE: not every row sees all of them.
-template <int DT, int D, bool BIAS, bool EDGE>
+// Probabilities of 32 keys, packed. edge: not every row sees all of them.
+template <int DT, int D, bool BIAS>
 __device__ __forceinline__ void weights_of(const HistoryArgs& a, float scale2, Wave<DT, D>& w, const BiasLds& sb,
-                                           float* win, const TileLane<D>& tl, const short* ks, int k0, int q0, int seen,
+                                           float* win, const TileLane<D>& tl, const short* ks, int k0, int q0, int seen, bool edge,
                                            s8v (&p)[2]) {
   const int lane = threadIdx.x & 63;
   Biases b{};
@@ -56,7 +56,7 @@ __device__ __forceinline__ void weights_of(const HistoryArgs& a, float scale2, W
     for (int i = 0; i < 16; ++i) s[0][i] = fmaf(s[0][i], scale2, at[8 * (i / 4) + i % 4]);
     mul = 1.f;
   }
-  if (EDGE) mask_tile(s[0], k0, seen);
+  if (edge) mask_tile(s[0], k0, seen);
   const float top = fmaf(both_halves_max(top_of(s)), mul, add);
   const bool up = top > w.mx + kSlack;
   if (__ballot(up)) {
@@ -138,15 +138,14 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
       const TileLane<D> tl = lanes.fresh();
       s8v p[2];
       float* win = s_win[BIAS ? wave : 0];
-      if (__builtin_expect(k + 32 <= seen_by_all, 1))
-        weights_of<DT, D, BIAS, false>(a, scale2, w, s_bias, win, tl, s_k[b] + 32 * n * D, k, q0, seen, p);
-      else if (k < seen_by_any)
-        weights_of<DT, D, BIAS, true>(a, scale2, w, s_bias, win, tl, s_k[b] + 32 * n * D, k, q0, seen, p);
+      const bool some = k < seen_by_any;
+      if (some)
+        weights_of<DT, D, BIAS>(a, scale2, w, s_bias, win, tl, s_k[b] + 32 * n * D, k, q0, seen, k + 32 > seen_by_all, p);
       if (__builtin_expect(special, 0)) {
         clear_special<DT, D>(vs, k, t.len, diagonal, &s_marks, 1);
         __syncthreads();
       }
-      if (k < seen_by_any) add_product<DT, D>(w.o, tl, vs, p);
+      if (some) add_product<DT, D>(w.o, tl, vs, p);
     }
   }
   if (!live) return;

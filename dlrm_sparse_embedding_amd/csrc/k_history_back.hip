@@ -100,11 +100,11 @@ __device__ __forceinline__ void pack_weights(const f16v& p, s8v (&x)[2]) {
   }
 }
 
-// P and dS of 32 keys, packed. EDGE: not every row sees all of them.
-template <int DT, int D, bool BIAS, bool EDGE>
+// P and dS of 32 keys, packed. edge: not every row sees all of them.
+template <int DT, int D, bool BIAS>
 __device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w, const BiasLds& sb, float* win,
                                            const TileLane<D>& tl, const short* ks, const short* vs, int k0, int q0,
-                                           int seen, s8v (&xp)[2], s8v (&xs)[2]) {
+                                           int seen, bool edge, s8v (&xp)[2], s8v (&xs)[2]) {
   const int lane = threadIdx.x & 63;
   Biases b{};
   if (BIAS) b = biases_of(p.a.f.h, sb, q0 + 31 - k0, win);
@@ -113,7 +113,6 @@ __device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w
   for (int i = 0; i < D / 16; ++i) s = mfma<DT>(tl.rows(ks, 0, i), w.q[i], s);
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(tl.rows(vs, 0, i), w.go[i], dp);
-  const uint32_t bits = EDGE ? row_bits(0, seen - k0) : 0;
   if (BIAS && !b.far) {
     const float* at = win + 4 * (lane >> 5) + 31 - (lane & 31);
 #pragma unroll
@@ -123,15 +122,22 @@ __device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w
 #pragma unroll
     for (int i = 0; i < 16; ++i) s[i] = fmaf(s[i], p.scale2, add);
   }
-  float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     s[i] = __builtin_amdgcn_exp2f(s[i]);
-    if (EDGE) s[i] = where_bit(bits, i, s[i]);
     dp[i] = s[i] * (dp[i] - w.delta);
-    if (EDGE) dp[i] = where_bit(bits, i, dp[i]);
-    sum += dp[i];
   }
+  if (edge) {
+    const uint32_t bits = row_bits(0, seen - k0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = where_bit(bits, i, s[i]);
+      dp[i] = where_bit(bits, i, dp[i]);
+    }
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum += dp[i];
   w.error += sum;
   w.c.fit(dp, w.dq);
   pack_weights<DT>(s, xp);
@@ -209,10 +215,8 @@ __global__ __launch_bounds__(256, D == 128 ? 1 : 2) void k_history_dq(BackDev p)
       const TileLane<D> tl = lanes.fresh();
       s8v xp[2], xs[2];
       float* win = s_win[BIAS ? wave : 0];
-      if (__builtin_expect(k + 32 <= seen_by_all, 1))
-        dq_weights<DT, D, BIAS, false>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, xp, xs);
-      else if (k < seen_by_any)
-        dq_weights<DT, D, BIAS, true>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, xp, xs);
+      if (k < seen_by_any)
+        dq_weights<DT, D, BIAS>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, k + 32 > seen_by_all, xp, xs);
       if (__builtin_expect(special, 0)) {
         __syncthreads();
         clear_special<DT, D>(ks, k, t.len, diagonal, nullptr, 0);
@@ -308,46 +312,26 @@ __device__ __forceinline__ void add_diagonals(const f16v& s, int row, float* sum
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 }
 
-// Scores' products of 32 queries (rows) and the wave's keys.
-template <int DT, int D>
-__device__ __forceinline__ void dkv_products(const KeyWave<DT, D>& w, const TileLane<D>& tl, const short* qs,
-                                             const short* gs, f16v& s, f16v& dp) {
-  s = f16v{};
-  dp = f16v{};
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) s = mfma<DT>(tl.rows(qs, 0, i), w.k[i], s);
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(tl.rows(gs, 0, i), w.v[i], dp);
-}
-
-// From the products to P (packed, scaled) and dS. bits: the rows that see the
-// lane's key, used where EDGE.
-template <int DT, bool BIAS, bool EDGE>
-__device__ __forceinline__ void dkv_weights(float scale2, const Biases& b, const float* win, const float* zs,
-                                            const float* deltas, uint32_t bits, f16v& s, const f16v& dp, s8v (&x)[2]) {
+// From the products to P (in s, and packed) and dS (in dp): NEAR with the biases of
+// each diagonal, else with `add` for all.
+template <int DT, bool NEAR>
+__device__ __forceinline__ void dkv_weights(float scale2, float add, const float* win, const float* zs,
+                                            const float* deltas, f16v& s, f16v& dp, s8v (&x)[2]) {
   const int lane = threadIdx.x & 63, h4 = 4 * (lane >> 5);
   // diagonal of (r, c): 31 - r + c
   const float* at = win + 31 - h4 + (lane & 31);
 #pragma unroll
   for (int i4 = 0; i4 < 16; i4 += 4) {
     const f4 z = *reinterpret_cast<const f4*>(zs + 2 * i4 + h4);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float add = !BIAS ? 0.f : b.far ? b.value : at[-(2 * i4 + j)];
-      float e = __builtin_amdgcn_exp2f(fmaf(s[i4 + j], scale2, add - z[j]));
-      s[i4 + j] = EDGE ? where_bit(bits, i4 + j, e) : e;
-    }
-  }
-  pack_weights<DT>(s, x);
-#pragma unroll
-  for (int i4 = 0; i4 < 16; i4 += 4) {
     const f4 delta = *reinterpret_cast<const f4*>(deltas + 2 * i4 + h4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float e = s[i4 + j] * (dp[i4 + j] - delta[j]);
-      s[i4 + j] = EDGE ? where_bit(bits, i4 + j, e) : e;
+      const float e = __builtin_amdgcn_exp2f(fmaf(s[i4 + j], scale2, (NEAR ? at[-(2 * i4 + j)] : add) - z[j]));
+      dp[i4 + j] = e * (dp[i4 + j] - delta[j]);
+      s[i4 + j] = e;
     }
   }
+  pack_weights<DT>(s, x);
 }
 
 // A tile's dS into the sums of the bias' gradient.
@@ -369,24 +353,102 @@ __device__ __forceinline__ void add_dbias(const BackDev& p, const Biases& b, con
   }
 }
 
-// P and dS of 32 queries from q0 on, packed. EDGE: not every key is seen by all of
-// them.
-template <int DT, int D, bool BIAS, bool EDGE>
+// P and dS of 32 queries from q0 on, packed. edge: not all of them see every key.
+template <int DT, int D, bool BIAS>
 __device__ __forceinline__ void dkv_step(const BackDev& p, KeyWave<DT, D>& w, const BiasLds& sb, float* win,
                                          GradLds<BIAS>& g, float (&far)[2], const TileLane<D>& tl, const short* qs,
                                          const short* gs, const float* zs, const float* deltas, int q0, int k0, int len,
-                                         s8v (&xp)[2], s8v (&xs)[2]) {
+                                         bool edge, s8v (&xp)[2], s8v (&xs)[2]) {
   Biases b{};
   if (BIAS) b = biases_of(p.a.f.h, sb, q0 + 31 - k0, win);
-  const int key = k0 + (threadIdx.x & 31);
-  // the rows that see the key; none sees one behind the end
-  const uint32_t bits = EDGE ? row_bits(p.a.f.h.causal ? key - q0 : 0, key < len ? len - q0 : 0) : 0;
-  f16v s, dp;
-  dkv_products<DT, D>(w, tl, qs, gs, s, dp);
-  dkv_weights<DT, BIAS, EDGE>(p.scale2, b, win, zs, deltas, bits, s, dp, xp);
-  add_dbias<BIAS>(p, b, s, g, far);
-  w.c.fit(s, w.dk);
-  pack_tile<DT>(w.c.scaled(s), xs);
+  uint32_t bits = 0;
+  if (edge) {  // none sees a key behind the end
+    const int key = k0 + (threadIdx.x & 31);
+    bits = row_bits(p.a.f.h.causal ? key - q0 : 0, key < len ? len - q0 : 0);
+  }
+  RowOps<D> qr, gr;
+  qr.read(tl, qs);
+  gr.read(tl, gs);
+  stage();
+  f16v s = qr.template times<DT>(w.k), dp = gr.template times<DT>(w.v);
+  if (BIAS && !b.far) dkv_weights<DT, true>(p.scale2, 0.f, win, zs, deltas, s, dp, xp);
+  else dkv_weights<DT, false>(p.scale2, b.value, win, zs, deltas, s, dp, xp);
+  if (edge) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = where_bit(bits, i, s[i]);
+      dp[i] = where_bit(bits, i, dp[i]);
+    }
+    pack_weights<DT>(s, xp);
+  }
+  add_dbias<BIAS>(p, b, dp, g, far);
+  w.c.fit(dp, w.dk);
+  pack_tile<DT>(w.c.scaled(dp), xs);
+}
+
+// 64 queries from q0 on, all of which see all keys. Products and vector work that
+// do not wait for each other stand side by side: the second half's scores with the
+// first half's P and dS, the first half's products with the second half's. NEAR:
+// with the biases of each distance, else of the last bucket or none.
+template <int DT, int D, bool BIAS, bool NEAR>
+__device__ __forceinline__ void dkv_pair(const BackDev& p, KeyWave<DT, D>& w, const BiasLds& sb, float (*win)[64],
+                                         GradLds<BIAS>& g, float (&far)[2], const TileLane<D>& tl, const short* qs,
+                                         const short* gs, const float* zs, const float* deltas, int q0, int k0) {
+  RowOps<D> qr, gr;
+  ColumnOps<D> gc, qc;
+  qr.read(tl, qs);
+  gr.read(tl, gs);
+  Biases b[2] = {};
+  if (BIAS) {
+    b[0] = biases_of(p.a.f.h, sb, q0 + 31 - k0, win[0], NEAR);
+    b[1] = biases_of(p.a.f.h, sb, q0 + 63 - k0, win[1], NEAR);
+  }
+  stage();
+  f16v s[2], dp[2];
+  s8v xp[2], xs[2][2];
+  s[0] = qr.template times<DT>(w.k);
+  qr.read(tl, qs + 32 * D);
+  dp[0] = gr.template times<DT>(w.v);
+  gr.read(tl, gs + 32 * D);
+  stage();
+  gc.read(tl, gs);
+  s[1] = qr.template times<DT>(w.k);
+  dp[1] = gr.template times<DT>(w.v);
+  dkv_weights<DT, NEAR>(p.scale2, b[0].value, win[0], zs, deltas, s[0], dp[0], xp);
+  interleave<D / 8, 8>();
+  stage();
+  if constexpr (DT != EMB_F16) {
+    qc.read(tl, qs);
+    pack_tile<DT>(dp[0], xs[0]);
+    gc.template times<DT>(w.dv, xp);
+    gc.read(tl, gs + 32 * D);
+    qc.template times<DT>(w.dk, xs[0]);
+    dkv_weights<DT, NEAR>(p.scale2, b[1].value, win[1], zs + 32, deltas + 32, s[1], dp[1], xp);
+    interleave<D / 8, 8>();
+    stage();
+    qc.read(tl, qs + 32 * D);
+    pack_tile<DT>(dp[1], xs[1]);
+    gc.template times<DT>(w.dv, xp);
+    qc.template times<DT>(w.dk, xs[1]);
+  } else {
+    // both halves' dS go by one scale, chosen when both are there
+    gc.template times<DT>(w.dv, xp);
+    gc.read(tl, gs + 32 * D);
+    dkv_weights<DT, NEAR>(p.scale2, b[1].value, win[1], zs + 32, deltas + 32, s[1], dp[1], xp);
+    interleave<D / 16, 16>();
+    stage();
+    qc.read(tl, qs);
+    gc.template times<DT>(w.dv, xp);
+    w.c.fit(dp[0], w.dk);
+    w.c.fit(dp[1], w.dk);
+    pack_tile<DT>(w.c.scaled(dp[0]), xs[0]);
+    pack_tile<DT>(w.c.scaled(dp[1]), xs[1]);
+    qc.template times<DT>(w.dk, xs[0]);
+    qc.read(tl, qs + 32 * D);
+    qc.template times<DT>(w.dk, xs[1]);
+  }
+  add_dbias<BIAS>(p, b[0], dp[0], g, far);
+  add_dbias<BIAS>(p, b[1], dp[1], g, far);
 }
 
 __device__ __forceinline__ float wave_sum(float x) {
@@ -400,13 +462,13 @@ __device__ __forceinline__ float wave_sum(float x) {
 // keys each, waves 2 and 3 the last 64, and are added to them at the end. So there
 // are twice as many blocks, half as long, as with 128 keys.
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p) {
+__global__ __launch_bounds__(256, 1) void k_history_dkv(BackDev p) {
   constexpr int kPart = kRows * D;  // elements of a tile
   __shared__ __attribute__((aligned(1024))) short s_tiles[4 * kPart];  // queries twice, dout twice
   __shared__ __attribute__((aligned(16))) float s_z[2][kRows], s_delta[2][kRows];
   __shared__ BiasLds s_bias;
   __shared__ GradLds<BIAS> s_grad;
-  __shared__ float s_win[BIAS ? 4 : 1][64];
+  __shared__ float s_win[BIAS ? 4 : 1][2][64];
   __shared__ Marks<D> s_marks;
   const HistoryArgs& a = p.a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -473,7 +535,19 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p)
       if (diagonal || q0 + kRows > t.len)
         special = any_special<DT, D>(qs, kRows) + any_special<DT, D>(gs, kRows) > 0;  // each has its barrier
       marked |= special;
-      float* win = s_win[BIAS ? wave : 0];
+      float(*wins)[64] = s_win[BIAS ? wave : 0];
+      if (__builtin_expect(!special && live && q0 + row0 + 64 <= t.len &&
+                               (a.h.causal ? q0 + row0 >= k0 + 31 : k0 + 32 <= t.len), 1)) {
+        const int q = q0 + row0;
+        const short *q_rows = qs + row0 * D, *g_rows = gs + row0 * D;
+        const float *zs = s_z[b] + row0, *deltas = s_delta[b] + row0;
+        if (BIAS && !all_far(a.h, q + 63 - k0, q - 31 - k0))
+          dkv_pair<DT, D, BIAS, BIAS>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
+        else
+          dkv_pair<DT, D, BIAS, false>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
+        continue;
+      }
+      float* win = wins[0];
 #pragma unroll 1
       for (int n = 0; n < 2; ++n) {
         const int r = row0 + 32 * n, q = q0 + r;
@@ -481,12 +555,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void k_history_dkv(BackDev p)
         s8v xp[2], xs[2];
         const bool some = live && q < t.len && !(a.h.causal && q + 31 < k0);
         const float *zs = s_z[b] + r, *deltas = s_delta[b] + r;
-        if (__builtin_expect(some && q + 32 <= t.len && (a.h.causal ? q >= k0 + 31 : k0 + 32 <= t.len), 1))
-          dkv_step<DT, D, BIAS, false>(p, w, s_bias, win, s_grad, far, tl, qs + r * D, gs + r * D, zs, deltas, q, k0,
-                                       t.len, xp, xs);
-        else if (some)
-          dkv_step<DT, D, BIAS, true>(p, w, s_bias, win, s_grad, far, tl, qs + r * D, gs + r * D, zs, deltas, q, k0,
-                                      t.len, xp, xs);
+        if (some)
+          dkv_step<DT, D, BIAS>(p, w, s_bias, win, s_grad, far, tl, qs + r * D, gs + r * D, zs, deltas, q, k0,
+                                t.len, q + 32 > t.len || (a.h.causal ? q < k0 + 31 : k0 + 32 > t.len), xp, xs);
         if (__builtin_expect(special, 0)) {
           __syncthreads();
           for (int half = 0; half < 2; ++half) {
