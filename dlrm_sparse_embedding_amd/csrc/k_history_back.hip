@@ -457,12 +457,15 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
+template <int D>
+constexpr bool kPairs = D > 64;
+
 // A block takes 64 keys of one key head and goes along the query tiles of 128 rows
 // of each of its query heads; waves 0 and 1 take the tiles' first 64 rows for 32
 // keys each, waves 2 and 3 the last 64, and are added to them at the end. So there
 // are twice as many blocks, half as long, as with 128 keys.
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, 1) void k_history_dkv(BackDev p) {
+__global__ __launch_bounds__(256, kPairs<D> ? 1 : 2) void k_history_dkv(BackDev p) {
   constexpr int kPart = kRows * D;  // elements of a tile
   __shared__ __attribute__((aligned(1024))) short s_tiles[4 * kPart];  // queries twice, dout twice
   __shared__ __attribute__((aligned(16))) float s_z[2][kRows], s_delta[2][kRows];
@@ -536,16 +539,18 @@ __global__ __launch_bounds__(256, 1) void k_history_dkv(BackDev p) {
         special = any_special<DT, D>(qs, kRows) + any_special<DT, D>(gs, kRows) > 0;  // each has its barrier
       marked |= special;
       float(*wins)[64] = s_win[BIAS ? wave : 0];
-      if (__builtin_expect(!special && live && q0 + row0 + 64 <= t.len &&
-                               (a.h.causal ? q0 + row0 >= k0 + 31 : k0 + 32 <= t.len), 1)) {
-        const int q = q0 + row0;
-        const short *q_rows = qs + row0 * D, *g_rows = gs + row0 * D;
-        const float *zs = s_z[b] + row0, *deltas = s_delta[b] + row0;
-        if (BIAS && !all_far(a.h, q + 63 - k0, q - 31 - k0))
-          dkv_pair<DT, D, BIAS, BIAS>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
-        else
-          dkv_pair<DT, D, BIAS, false>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
-        continue;
+      if constexpr (kPairs<D>) {
+        if (__builtin_expect(!special && live && q0 + row0 + 64 <= t.len &&
+                                 (a.h.causal ? q0 + row0 >= k0 + 31 : k0 + 32 <= t.len), 1)) {
+          const int q = q0 + row0;
+          const short *q_rows = qs + row0 * D, *g_rows = gs + row0 * D;
+          const float *zs = s_z[b] + row0, *deltas = s_delta[b] + row0;
+          if (BIAS && !all_far(a.h, q + 63 - k0, q - 31 - k0))
+            dkv_pair<DT, D, BIAS, BIAS>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
+          else
+            dkv_pair<DT, D, BIAS, false>(p, w, s_bias, wins, s_grad, far, lanes.fresh(), q_rows, g_rows, zs, deltas, q, k0);
+          continue;
+        }
       }
       float* win = wins[0];
 #pragma unroll 1
