@@ -145,7 +145,7 @@ __device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w
 }
 
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, D == 128 ? 1 : 2) void k_history_dq(BackDev p) {
+__global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
   __shared__ __attribute__((aligned(1024))) short s_k[2][kTile * D], s_v[2][kTile * D];
   __shared__ BiasLds s_bias;
   __shared__ float s_win[BIAS ? 4 : 1][64];
