@@ -457,15 +457,20 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-template <int D>
-constexpr bool kPairs = D > 64;
+// Whole tiles in pairs of half tiles, with one block a CU, or every half tile by
+// itself. The gradient of 12289 items, 16 x 4 heads, with a bias: 128 wide bf16
+// 1657 us in pairs and 1922 without; fp16, whose pairs take one scale and with it
+// more registers than there are, 2600 and 1705; 64 wide, where two blocks fit
+// without pairs, 696 and 632 (no bias).
+template <int DT, int D>
+constexpr bool kPairs = D > 64 && DT == EMB_BF16;
 
 // A block takes 64 keys of one key head and goes along the query tiles of 128 rows
 // of each of its query heads; waves 0 and 1 take the tiles' first 64 rows for 32
 // keys each, waves 2 and 3 the last 64, and are added to them at the end. So there
 // are twice as many blocks, half as long, as with 128 keys.
 template <int DT, int D, bool BIAS>
-__global__ __launch_bounds__(256, kPairs<D> ? 1 : 2) void k_history_dkv(BackDev p) {
+__global__ __launch_bounds__(256, D > 64 ? 1 : 2) void k_history_dkv(BackDev p) {
   constexpr int kPart = kRows * D;  // elements of a tile
   __shared__ __attribute__((aligned(1024))) short s_tiles[4 * kPart];  // queries twice, dout twice
   __shared__ __attribute__((aligned(16))) float s_z[2][kRows], s_delta[2][kRows];
@@ -539,7 +544,7 @@ __global__ __launch_bounds__(256, kPairs<D> ? 1 : 2) void k_history_dkv(BackDev 
         special = any_special<DT, D>(qs, kRows) + any_special<DT, D>(gs, kRows) > 0;  // each has its barrier
       marked |= special;
       float(*wins)[64] = s_win[BIAS ? wave : 0];
-      if constexpr (kPairs<D>) {
+      if constexpr (kPairs<DT, D>) {
         if (__builtin_expect(!special && live && q0 + row0 + 64 <= t.len &&
                                  (a.h.causal ? q0 + row0 >= k0 + 31 : k0 + 32 <= t.len), 1)) {
           const int q = q0 + row0;
