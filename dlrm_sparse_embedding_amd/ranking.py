@@ -18,14 +18,49 @@ import torch
 from . import emb as E
 
 
-class HistoryRanker:
+class Pages:
+    """A paged cache and who has its pages."""
+
+    def hold_cache(self, pages: int, page: int, kv_heads: int, dim: int, dtype) -> None:
+        shape = (pages, kv_heads, page, dim)       # a page holds each head's rows together
+        self.page = page
+        self.cache = E.KVCache(torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2),
+                               torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2))
+        self.next_page = 0        # pages from here on were never handed out
+        self.returned = []        # pages handed back
+
+    def new_pages(self, counts) -> torch.Tensor:
+        """A page table row for each of `counts` slots; -1 behind the last page."""
+        need = [-(-int(c) // self.page) for c in counts]
+        if sum(need) > len(self.returned) + self.cache.pages - self.next_page:
+            raise ValueError("the cache has no pages left")
+        table = torch.full((len(need), max(need + [1])), -1, dtype=torch.int32)
+        for row, n in zip(table, need):
+            again = min(n, len(self.returned))
+            if again:
+                row[:again] = torch.tensor(self.returned[-again:], dtype=torch.int32)
+                del self.returned[-again:]
+            row[again:n] = torch.arange(self.next_page, self.next_page + n - again, dtype=torch.int32)
+            self.next_page += n - again
+        return table.cuda()
+
+    def return_pages(self, table) -> None:
+        """Hands back the pages of new_pages' table rows, for later rows. Work on them has to be done, or under way
+        on the stream that will use them next."""
+        pages = [p for p in table.flatten().tolist() if p >= 0]
+        if len(set(pages)) != len(pages) or any(p >= self.next_page for p in pages) or set(pages) & set(self.returned):
+            raise ValueError("a page that is not handed out")
+        self.returned += pages
+
+
+class HistoryRanker(Pages):
     """One attention layer over embedded items. Positions are places in a history; a candidate takes the place
     after its last item. With ``norm`` queries and keys are normed per head, otherwise only turned."""
 
     def __init__(self, items: int, width: int = 64, heads: int = 8, kv_heads: int = 2, dim: int = 64,
                  pages: int = 1024, page: int = 16, norm: bool = True, layout: str = "half", seed: int = 0,
                  dtype=torch.bfloat16):
-        self.heads, self.kv_heads, self.dim, self.page, self.eps = heads, kv_heads, dim, page, 1e-6
+        self.heads, self.kv_heads, self.dim, self.eps = heads, kv_heads, dim, 1e-6
         self.dtype = dtype
         self.tables = E.EmbeddingTables([E.TableSpec(items, width, "f32")], with_state=True)
         self.tables.init_uniform(seed)
@@ -39,11 +74,7 @@ class HistoryRanker:
         self.wk = torch.ones(dim, device="cuda") if norm else None
         self.norm = norm
         self.rotary = E.Rotary(dim, layout=layout)
-        shape = (pages, kv_heads, page, dim)       # a page holds each head's rows together
-        self.cache = E.KVCache(torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2),
-                               torch.zeros(shape, dtype=dtype, device="cuda").transpose(1, 2))
-        self.next_page = 0        # pages from here on were never handed out
-        self.returned = []        # pages handed back
+        self.hold_cache(pages, page, kv_heads, dim, dtype)
 
     def close(self) -> None:
         self.tables.close()
@@ -77,29 +108,6 @@ class HistoryRanker:
         return qo, ko
 
     # ---- serving ----
-
-    def new_pages(self, counts) -> torch.Tensor:
-        """A page table row for each of `counts` slots; -1 behind the last page."""
-        need = [-(-int(c) // self.page) for c in counts]
-        if sum(need) > len(self.returned) + self.cache.pages - self.next_page:
-            raise ValueError("the cache has no pages left")
-        table = torch.full((len(need), max(need + [1])), -1, dtype=torch.int32)
-        for row, n in zip(table, need):
-            again = min(n, len(self.returned))
-            if again:
-                row[:again] = torch.tensor(self.returned[-again:], dtype=torch.int32)
-                del self.returned[-again:]
-            row[again:n] = torch.arange(self.next_page, self.next_page + n - again, dtype=torch.int32)
-            self.next_page += n - again
-        return table.cuda()
-
-    def return_pages(self, table) -> None:
-        """Hands back the pages of new_pages' table rows, for later rows. Work on them has to be done, or under way
-        on the stream that will use them next."""
-        pages = [p for p in table.flatten().tolist() if p >= 0]
-        if len(set(pages)) != len(pages) or any(p >= self.next_page for p in pages) or set(pages) & set(self.returned):
-            raise ValueError("a page that is not handed out")
-        self.returned += pages
 
     def append(self, ids, offsets, lens, table, positions=None) -> None:
         """Writes the items' keys and values to their sequences' pages (offsets, lens, table: emb_kv_append)."""
