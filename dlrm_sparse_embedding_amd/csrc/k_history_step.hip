@@ -7,7 +7,9 @@
 // into registers, values through the wave's own LDS tile, both a tile ahead, and
 // their pages are looked up another tile ahead. Long histories are split into
 // parts, which a second launch joins with the weights 2^(z_i - max z). It is bound
-// by reading the slots once.
+// by reading the slots once: 61 users of up to 3000 slots, 32 x 8 heads of 128
+// bf16, 76 us, 5.5 TB/s; one user of 60001, 16 x 4 heads of 64 fp16, 20 us, of
+// which the join is 5 and the rest bound by dependent reads (length, page, slot).
 #include <algorithm>
 
 #include "history_device.h"
@@ -72,9 +74,11 @@ __global__ __launch_bounds__(256, 2) void k_history_step(StepDev p) {
       s.page = 0;  // in range; what it holds is meaningless
     }
     const short* kp = reinterpret_cast<const short*>(kv.k) + s.page * kv.kps + s.in_page * kv.kss + h * kv.khs;
+    // four loads take a line together: they leave it to the caches, unlike those of
+    // values (61 users, 8 heads of 128: 118 us with nontemporal ones, now 76)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
-      kf[i] = __builtin_nontemporal_load(reinterpret_cast<const s8v*>(kp + 16 * i + 8 * (lane >> 5)));
+      kf[i] = *reinterpret_cast<const s8v*>(kp + 16 * i + 8 * (lane >> 5));
 #pragma unroll
     for (int i = 0; i < kPieces<D>; ++i) {
       const int piece = i * 64 + lane, row = piece / (D / 8);
@@ -231,13 +235,15 @@ __global__ __launch_bounds__(256, 2) void k_history_step(StepDev p) {
           f4{o[d][4 * i] * inv, o[d][4 * i + 1] * inv, o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv};
 }
 
-// Joins the parts of each (sequence, query head): 32 lanes, 4 columns each.
-template <int DT, int D>
+// Joins the parts of each (sequence, query head). A row is taken by GROUPS (1 or 8)
+// groups of 32 lanes, 4 columns a lane, each of which takes every GROUPS-th set of
+// eight parts (128 parts of 16 rows of 64: 17.7 us with one, 5.2 with eight).
+template <int DT, int D, int GROUPS>
 __global__ __launch_bounds__(256) void k_history_join(StepDev p) {
   const HistoryStepArgs& a = p.a;
-  const int l = threadIdx.x & 31;
+  const int l = threadIdx.x & 31, group = threadIdx.x >> 5;
   const long long rows = (long long)a.seqs * a.h.q_heads;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long row = GROUPS == 1 ? (long long)blockIdx.x * 8 + group : blockIdx.x;
   if (row >= rows) return;
   float z[kMaxParts / 32], top = kNegInf;
 #pragma unroll
@@ -260,7 +266,8 @@ __global__ __launch_bounds__(256) void k_history_join(StepDev p) {
   // eight parts' loads at once; an empty part holds nothing, not zeros
 #pragma unroll
   for (int g = 0; g < kMaxParts / 32; ++g)
-    for (int i = 32 * g; i < min(a.parts, 32 * g + 32); i += 8) {
+    for (int i = 32 * g + (GROUPS == 1 ? 0 : 8 * (group & 3)); i < min(a.parts, 32 * g + 32); i += GROUPS == 1 ? 8 : 32) {
+      if (GROUPS > 1 && (g & 1) != (group >> 2)) continue;
       f4 x[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -271,6 +278,14 @@ __global__ __launch_bounds__(256) void k_history_join(StepDev p) {
         if (i + k < a.parts && w != 0.f) acc += x[k] * w;
       }
     }
+  if constexpr (GROUPS > 1) {
+    __shared__ f4 s_acc[GROUPS][32];
+    s_acc[group][l] = acc;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 1; g < GROUPS; ++g) acc += s_acc[g][l];
+  }
   const bool some = !(total == 0.f);
   const float inv = some ? 1.f / total : 0.f;
   const long long b = row / a.h.q_heads;
@@ -290,14 +305,18 @@ hipError_t launch(const StepDev& p, hipStream_t st) {
   else k_history_step<DT, D, false><<<blocks, 256, 0, st>>>(p);
   if (hipError_t e = hipGetLastError()) return e;
   if (a.parts == 1) return hipSuccess;
-  k_history_join<DT, D><<<(unsigned)(((long long)a.seqs * a.h.q_heads + 7) / 8), 256, 0, st>>>(p);
+  // many parts are those of few sequences
+  const long long rows = (long long)a.seqs * a.h.q_heads;
+  if (a.parts > 16) k_history_join<DT, D, 8><<<(unsigned)rows, 256, 0, st>>>(p);
+  else k_history_join<DT, D, 1><<<(unsigned)((rows + 7) / 8), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
 // Parts of the slots: two blocks for each CU at least, but none below 256 slots,
-// since each part writes and reads back an fp32 partial output.
+// since each part writes and reads back an fp32 partial output. (61 users' 488
+// pairs with a head: 118 us for at least 1024 blocks, 128 for 600, 124 for 2048.)
 int history_step_parts(const HistoryView& h, const KvView& kv, int seqs, int width) {
   const long long items = (long long)seqs * h.kv_heads, cap = (long long)width * kv.page;
   if (items == 0) return 1;
