@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <new>
 
 #include "emb.h"
@@ -104,14 +105,20 @@ Buckets make_buckets(const emb_history_desc& d) {
   return b;
 }
 
+// A launch has less than 2^32 threads, that is 2^24 blocks of 256.
+constexpr long long kMaxBlocks = 1ll << 24;
+
+bool too_many(const HistoryView& h, long long tokens, int seqs) {
+  return (seqs + tokens / 64) * h.q_heads >= kMaxBlocks || tokens * h.q_heads >= (1ll << 31);
+}
+
 // Sequences of a call on ragged operands.
 int check_ragged(const emb_history* h, int64_t tokens, const int32_t* offsets, int32_t seqs, const float* bias) {
   if (!h) return fail(EMB_E_INVAL, "history is NULL");
   if (tokens < 0 || tokens >= (1ll << 24)) return fail(EMB_E_INVAL, "tokens %lld not in [0, 2^24)", (long long)tokens);
   if (seqs < 0 || seqs >= (1 << 24)) return fail(EMB_E_INVAL, "seqs %d not in [0, 2^24)", seqs);
   if (seqs == 0 && tokens > 0) return fail(EMB_E_INVAL, "tokens without a sequence");
-  if ((seqs + tokens / 64) * h->v.q_heads >= (1ll << 30) || tokens * h->v.q_heads >= (1ll << 31))
-    return fail(EMB_E_INVAL, "too many tokens or sequences for one call");
+  if (too_many(h->v, tokens, seqs)) return fail(EMB_E_INVAL, "too many tokens or sequences for one call");
   if (h->v.buckets.n > 0 && (!bias || !aligned(bias, 4))) return fail(EMB_E_INVAL, "bias is NULL or misaligned");
   if (h->v.buckets.n == 0 && bias) return fail(EMB_E_INVAL, "bias without buckets");
   if (tokens > 0 && (!offsets || !aligned(offsets, 4))) return fail(EMB_E_INVAL, "offsets are NULL or misaligned");
@@ -124,6 +131,13 @@ int check_wide(const char* name, const Heads& x, long long tokens, const History
   if (!aligned(x.p, 16) || x.ts % 8 != 0 || x.hs % 8 != 0)
     return fail(EMB_E_INVAL, "%s needs 16-byte alignment and strides of multiples of 16 bytes", name);
   if (x.ts >= (1ll << 24)) return fail(EMB_E_INVAL, "%s: a token stride of 2^24 elements or more", name);
+  return EMB_OK;
+}
+
+// A written operand that starts where one that other blocks read does.
+int check_apart(const char* name, const Heads& out, std::initializer_list<Heads> others) {
+  for (const Heads& o : others)
+    if (o.p == out.p) return fail(EMB_E_INVAL, "%s is another operand's memory", name);
   return EMB_OK;
 }
 
@@ -148,7 +162,8 @@ int check_step(const emb_history* history, const emb_kv* kv, int32_t seqs, int32
   if (!aligned(c.k, 16) || !aligned(c.v, 16)) return fail(EMB_E_INVAL, "the cache is not 16-byte aligned");
   if (seqs < 0 || seqs >= (1 << 24)) return fail(EMB_E_INVAL, "seqs %d not in [0, 2^24)", seqs);
   if (width < 0 || (long long)width * c.page >= (1ll << 30)) return fail(EMB_E_INVAL, "a page table row holds 2^30 slots or more");
-  if ((long long)seqs * h.q_heads >= (1ll << 28)) return fail(EMB_E_INVAL, "too many sequences for one call");
+  if ((long long)seqs * h.kv_heads >= kMaxBlocks / 2 || (long long)seqs * h.q_heads >= (1ll << 28))
+    return fail(EMB_E_INVAL, "too many sequences for one call");
   return EMB_OK;
 }
 
@@ -280,7 +295,8 @@ int emb_history_attention(emb_history* history, int64_t tokens, const void* q, i
                       {k, k_token_stride, k_head_stride, h.kv_heads}, {v, v_token_stride, v_head_stride, h.kv_heads},
                       {out, out_token_stride, out_head_stride, h.q_heads}, offsets, bias, lse};
   if ((rc = check_wide("q", a.q, tokens, h, false)) || (rc = check_wide("k", a.k, tokens, h, false)) ||
-      (rc = check_wide("v", a.v, tokens, h, false)) || (rc = check_wide("out", a.out, tokens, h, true)))
+      (rc = check_wide("v", a.v, tokens, h, false)) || (rc = check_wide("out", a.out, tokens, h, true)) ||
+      (rc = check_apart("out", a.out, {a.k, a.v})))
     return rc;
   hipError_t e = launch_history(a, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return hip_fail(e, "attention of histories");
@@ -289,6 +305,7 @@ int emb_history_attention(emb_history* history, int64_t tokens, const void* q, i
 
 size_t emb_history_attention_workspace_bytes(const emb_history* history, int64_t tokens, int32_t seqs) {
   if (!history || tokens < 0 || tokens >= (1ll << 24) || seqs < 0 || seqs >= (1 << 24)) return 0;
+  if (too_many(history->v, tokens, seqs)) return 0;
   return history_back_plan(history->v, tokens, seqs).bytes;
 }
 
@@ -323,6 +340,10 @@ int emb_history_attention_backward(emb_history* history, int64_t tokens, const v
     if (!lse || !aligned(lse, 4)) return fail(EMB_E_INVAL, "lse is NULL or misaligned");
     const HistoryBackPlan p = history_back_plan(h, tokens, seqs);
     if ((rc = check_workspace(ws, ws_bytes, p.bytes))) return rc;
+    if ((rc = check_apart("dq", a.dq, {a.f.q, a.f.k, a.f.v, a.f.out, a.dout, a.dk, a.dv})) ||
+        (rc = check_apart("dk", a.dk, {a.f.q, a.f.k, a.f.v, a.f.out, a.dout, a.dv})) ||
+        (rc = check_apart("dv", a.dv, {a.f.q, a.f.k, a.f.v, a.f.out, a.dout})))
+      return rc;
     a.rows = static_cast<float*>(ws);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_off);
   }

@@ -506,3 +506,22 @@ def test_step_in_a_graph_on_other_streams():
         s.run(stream=torch.cuda.Stream())
         torch.cuda.synchronize()
         assert torch.equal(got, s.out)
+
+
+def test_nearly_as_many_sequences_as_a_launch_takes():
+    """A million sequences, three of which have tokens: the bits of those three alone."""
+    lens, at, n = [50, 1, 130], [5, 777_777, 1_040_000], 1_045_000
+    a = Call("bf16", 64, 16, 16, lens)
+    where = torch.zeros(n, dtype=torch.int32)
+    where[at] = torch.tensor(lens, dtype=torch.int32)
+    many = torch.cat([torch.zeros(1, dtype=torch.int32), where.cumsum(0).to(torch.int32)]).cuda()
+    assert (n + sum(lens) // 64) * 16 < 1 << 24 <= (n + 5000) * 16
+    a.forward()
+    want = [t.clone() for t in [a.out, a.lse] + a.backward()]
+    a.offsets = many
+    a.ws = torch.empty(E.emb_history_attention_workspace_bytes(a.h.handle, a.T, n), dtype=torch.uint8, device="cuda")
+    for t in (a.out, a.lse, a.dq, a.dk, a.dv):
+        t.fill_(3)
+    a.forward()
+    assert all(torch.equal(x, y) for x, y in zip(want, [a.out, a.lse] + a.backward()))
+    a.h.check_error()

@@ -227,3 +227,36 @@ def test_history_step_without_sequences():
     assert rc_of("emb_history_step", dict(STEP, h=h, kv=c), dict(seqs=0, q=None, lens=None, ws=None)) == OK
     E.emb_destroy_history(h)
     E.emb_destroy_kv(c)
+
+
+def test_history_calls_beyond_one_launch():
+    """A launch has less than 2^24 blocks of 256 threads."""
+    h, c = handle(), cache()            # 8 query heads, 2 of the cache
+    back, step = E.emb_history_attention_workspace_bytes, E.emb_history_step_workspace_bytes
+    hq = DESC["hq"]
+    most = (1 << 24) // hq - 1
+    for seqs, good in ((most, True), (most + 1, False)):
+        assert (back(h, 10, seqs) > 0) == good
+        if not good:
+            assert rc_of("emb_history_attention", dict(ATT, h=h), dict(seqs=seqs)) == INVAL
+            assert rc_of("emb_history_attention_backward", dict(BACK_ATT, h=h), dict(seqs=seqs, n=1 << 60)) == INVAL
+    most = (1 << 23) // 2 - 1
+    assert step(h, c, most, 8) >= 16 and step(h, c, most + 1, 8) == 0
+    assert rc_of("emb_history_step", dict(STEP, h=h, kv=c), dict(seqs=most + 1, n=1 << 60)) == INVAL
+    E.emb_destroy_history(h)
+    E.emb_destroy_kv(c)
+
+
+def test_history_operands_that_share_memory():
+    """What is written must not start where another operand that is read, or written, does."""
+    h = handle()
+    apart = {n: FAKE + 4096 * i for i, n in enumerate(("q", "k", "v", "out", "dout", "dq", "dk", "dv"))}
+    few = {n: apart[n] for n in ("q", "k", "v", "out")}
+    for other in ("k", "v"):
+        assert rc_of("emb_history_attention", dict(ATT, h=h, **few), dict(out=apart[other])) == INVAL
+    for written in ("dq", "dk", "dv"):
+        for other in apart:
+            if other != written:
+                assert rc_of("emb_history_attention_backward", dict(BACK_ATT, h=h, **apart),
+                             {written: apart[other]}) == INVAL
+    E.emb_destroy_history(h)
