@@ -8,7 +8,7 @@
 // their pages are looked up another tile ahead. Long histories are split into
 // parts, which a second launch joins with the weights 2^(z_i - max z). It is bound
 // by reading the slots once: 61 users of up to 3000 slots, 32 x 8 heads of 128
-// bf16, 76 us, 5.5 TB/s; one user of 60001, 16 x 4 heads of 64 fp16, 20 us, of
+// bf16, 90 us, 4.6 TB/s (76 where a part of them is still in the last cache); one user of 60001, 16 x 4 heads of 64 fp16, 20 us, of
 // which the join is 5 and the rest bound by dependent reads (length, page, slot).
 #include <algorithm>
 
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256, 2) void k_history_step(StepDev p) {
     }
     const short* kp = reinterpret_cast<const short*>(kv.k) + s.page * kv.kps + s.in_page * kv.kss + h * kv.khs;
     // four loads take a line together: they leave it to the caches, unlike those of
-    // values (61 users, 8 heads of 128: 118 us with nontemporal ones, now 76)
+    // values (61 users, 8 heads of 128: 119 us with nontemporal ones, now 90)
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
       kf[i] = *reinterpret_cast<const s8v*>(kp + 16 * i + 8 * (lane >> 5));
