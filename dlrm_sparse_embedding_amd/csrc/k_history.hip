@@ -15,8 +15,9 @@
 //
 // Bound by the products and the vector work of a wave, which overlap with another
 // wave's only in part: 12289 items, 16 x 4 heads of 128, causal, 270 us without a
-// bias (860 TFLOP/s), 360 with one of 64 buckets up to 1024, where half of the
-// tiles have a bias for each diagonal; heads of 64 165 us (710 TFLOP/s: as many
+// bias (860 TFLOP/s), 305 with one of 64 buckets up to 1024, where a third of the
+// tiles have a bias for each diagonal (297 with the biases of all near distances in
+// a table, whose kernels for the gradient are slower); heads of 64 165 us (710 TFLOP/s: as many
 // exponentials for half the products). Waits that the compiler puts into the loop
 // (operands not there before it, spilled registers) also wait for the next tile's
 // transfer: without them the long cases went from 1137 to 1090 us.
