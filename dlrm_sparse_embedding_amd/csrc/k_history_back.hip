@@ -108,9 +108,16 @@ __device__ __forceinline__ void pack_weights(const f16v& p, s8v (&x)[2]) {
   }
 }
 
+// How many pieces of a lane's dout stay in LDS: with a bias and 128-wide heads there
+// are that many registers too few, and a spilled one is fetched by a load that waits
+// for the tile in flight.
+template <int D, bool BIAS>
+constexpr int kHeld = BIAS && D == 128 ? 3 : 0;
+
 // P and dS of 32 keys, packed. edge: not every row sees all of them.
 template <int DT, int D, bool BIAS>
-__device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w, const BiasLds& sb, float* win,
+__device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w, const s8v (*held)[256],
+                                           const BiasLds& sb, float* win,
                                            const TileLane<D>& tl, const short* ks, const short* vs, int k0, int q0,
                                            int seen, bool edge, s8v (&xp)[2], s8v (&xs)[2]) {
   const int lane = threadIdx.x & 63;
@@ -120,7 +127,8 @@ __device__ __forceinline__ void dq_weights(const BackDev& p, QueryWave<DT, D>& w
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) s = mfma<DT>(tl.rows(ks, 0, i), w.q[i], s);
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) dp = mfma<DT>(tl.rows(vs, 0, i), w.go[i], dp);
+  for (int i = 0; i < D / 16; ++i)
+    dp = mfma<DT>(tl.rows(vs, 0, i), i < kHeld<D, BIAS> ? held[i][threadIdx.x] : w.go[i], dp);
   if (BIAS && !b.far) {
     const float* at = win + 4 * (lane >> 5) + 31 - (lane & 31);
 #pragma unroll
@@ -157,6 +165,7 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
   __shared__ __attribute__((aligned(1024))) short s_k[2][kTile * D], s_v[2][kTile * D];
   __shared__ BiasLds s_bias;
   __shared__ float s_win[BIAS ? 4 : 1][64];
+  __shared__ s8v s_held[kHeld<D, BIAS> > 0 ? kHeld<D, BIAS> : 1][256];
   const HistoryArgs& a = p.a.f;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   report_offsets(a.offsets, a.seqs, a.tokens, a.h.error);
@@ -200,6 +209,8 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
     }
     w.delta = both_halves_sum(dot);
   }
+#pragma unroll
+  for (int i = 0; i < kHeld<D, BIAS>; ++i) s_held[i][threadIdx.x] = w.go[i];  // each lane reads its own
   w.z = z_of(a.lse[token * a.h.q_heads + head]);
   w.error = 0.f;
 #pragma unroll
@@ -224,7 +235,7 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
       s8v xp[2], xs[2];
       float* win = s_win[BIAS ? wave : 0];
       if (k < seen_by_any)
-        dq_weights<DT, D, BIAS>(p, w, s_bias, win, tl, ks, vs, k, q0, seen, k + 32 > seen_by_all, xp, xs);
+        dq_weights<DT, D, BIAS>(p, w, s_held, s_bias, win, tl, ks, vs, k, q0, seen, k + 32 > seen_by_all, xp, xs);
       if (__builtin_expect(special, 0)) {
         __syncthreads();
         clear_special<DT, D>(ks, k, t.len, diagonal, nullptr, 0);
