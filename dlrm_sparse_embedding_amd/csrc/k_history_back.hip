@@ -265,6 +265,14 @@ __global__ __launch_bounds__(256, 2) void k_history_dq(BackDev p) {
   for (int d = 0; d < D / 32; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) w.dq[d][i] = w.dq[d][i] * by - off * w.pk[d][i];
+  // the only key that a row sees has P = 1 and dS = 0, and what the rounding of dS
+  // left of dq against its correction is all that there is
+  if (a.h.causal ? place == 0 : t.len == 1) {
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w.dq[d][i] -= w.dq[d][i];  // a NaN stays one
+  }
   short* dst = reinterpret_cast<short*>(const_cast<void*>(p.a.dq.p)) + token * p.a.dq.ts + head * p.a.dq.hs +
                8 * (lane >> 5);
   store_columns<DT, D>(dst, w.dq, a.h.scale, store);

@@ -525,3 +525,24 @@ def test_nearly_as_many_sequences_as_a_launch_takes():
     a.forward()
     assert all(torch.equal(x, y) for x, y in zip(want, [a.out, a.lse] + a.backward()))
     a.h.check_error()
+
+
+@pytest.mark.parametrize("dt,dim", [("bf16", 64), ("f16", 64), ("bf16", 96), ("f16", 96), ("bf16", 128), ("f16", 128)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("spec", [SPEC, None])
+def test_one_key_has_no_gradient_of_scores(dt, dim, causal, spec):
+    """A softmax over one key is constant: zero gradients of queries, keys and biases, exactly; also of the first
+    rows of longer causal histories."""
+    c = Call(dt, dim, 4, 2, [1] * 37, causal, spec)
+    c.forward()
+    c.backward()
+    assert not c.dq.any() and not c.dk.any() and (spec is None or not c.dbias.any())
+    c.check_forward()
+    c.check_backward()
+    if causal:
+        c = Call(dt, dim, 4, 2, [70, 3], causal, spec)
+        c.forward()
+        c.backward()
+        assert not c.dq[0].any() and not c.dq[70].any() and c.dq[1].any()
+        c.check_forward()
+        c.check_backward()
