@@ -8,7 +8,6 @@ namespace emb {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kHidden = -0x1p100f;  // entries of the bias from here down hide their distances
 
 // ---- tiles in LDS -------------------------------------------------------------
 // 64 rows of D elements without padding; 16-byte piece c of row r lies at c ^
@@ -170,7 +169,7 @@ __device__ __forceinline__ int bias_row(const HistoryView& h, const int* first, 
   return d < 0 ? g + h.buckets.n : g;
 }
 // A bias as the kernels use it: in units of log2, minus infinity where it hides.
-__device__ __forceinline__ float bias_log2(float b) { return b <= kHidden ? kNegInf : b * kLog2e; }
+__device__ __forceinline__ float bias_log2(float b) { return b <= EMB_HIDDEN_BIAS ? kNegInf : b * kLog2e; }
 
 // A block's copy of the bounds and of one head's bias.
 struct BiasLds {

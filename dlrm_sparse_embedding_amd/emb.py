@@ -98,6 +98,7 @@ class emb_kv_desc(ctypes.Structure):
 
 EMB_MAX_ROW_DIM = 16384
 EMB_MAX_BUCKETS = 128
+EMB_HIDDEN_BIAS = -8192.0
 
 
 class emb_history_desc(ctypes.Structure):

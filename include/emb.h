@@ -738,10 +738,13 @@ int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t
  * causal, buckets + bucket(-d) for d < 0, so the table has `buckets` rows or 2
  * buckets (row `buckets` is then never used). exact = buckets: distances beyond
  * buckets - 1 share the last bucket, far is not used. buckets = 0: no bias.
- * An entry at or below -2^100 (-infinity, the type's lowest value) hides its
- * distances: their keys are not seen. A query that sees no key gets zeros and
- * -infinity, and its gradients are zeros. Other entries and the scores must
- * stay below 2^100 in magnitude.
+ * An entry at or below EMB_HIDDEN_BIAS (-infinity, a 16- or 32-bit type's
+ * lowest value, -1e4, -1e9) hides its distances: their keys are not seen. A
+ * query that sees no key gets zeros and -infinity, and its gradients are zeros.
+ * Other entries and the scores must stay below -EMB_HIDDEN_BIAS in magnitude:
+ * the gradient makes its weights from s and lse, whose fp32 roundings put them
+ * off by up to 6 * 2^-24 |s| relative, which at that magnitude is less than
+ * half a step of bf16, and far beyond it any number.
  * Tokens that a query does not see have no influence on its row, whatever they
  * hold (other sequences', later ones'), except that hidden keys' infinities
  * enter products with a weight of 0. Reruns are bit-identical.
@@ -764,6 +767,7 @@ typedef struct emb_history_desc {
 } emb_history_desc;
 
 #define EMB_MAX_BUCKETS 128
+#define EMB_HIDDEN_BIAS (-8192.0f)
 
 typedef struct emb_history emb_history;
 

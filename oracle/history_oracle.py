@@ -68,7 +68,7 @@ def dropout(x, residual, p, seed, step):
 
 # ---- attention ----------------------------------------------------------------
 
-HIDDEN = -2.0 ** 100
+HIDDEN = -2.0 ** 13
 
 
 def bucket(d, buckets, exact, far):
