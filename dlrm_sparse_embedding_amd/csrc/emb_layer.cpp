@@ -141,6 +141,14 @@ int check_apart(const char* name, const Heads& out, std::initializer_list<Heads>
   return EMB_OK;
 }
 
+// out may be q with the same strides: a block reads its queries before it writes their rows, and no other block reads
+// them. Strides over one token or one head do not count.
+int check_in_q(const Heads& q, const Heads& out, long long tokens) {
+  if (q.p == out.p && ((tokens > 1 && q.ts != out.ts) || (q.n > 1 && q.hs != out.hs)))
+    return fail(EMB_E_INVAL, "out is q with other strides");
+  return EMB_OK;
+}
+
 int check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(EMB_E_INVAL, "ws is NULL");
   if (!aligned(ws, 16)) return fail(EMB_E_INVAL, "ws is not 16-byte aligned");
@@ -296,7 +304,7 @@ int emb_history_attention(emb_history* history, int64_t tokens, const void* q, i
                       {out, out_token_stride, out_head_stride, h.q_heads}, offsets, bias, lse};
   if ((rc = check_wide("q", a.q, tokens, h, false)) || (rc = check_wide("k", a.k, tokens, h, false)) ||
       (rc = check_wide("v", a.v, tokens, h, false)) || (rc = check_wide("out", a.out, tokens, h, true)) ||
-      (rc = check_apart("out", a.out, {a.k, a.v})))
+      (rc = check_apart("out", a.out, {a.k, a.v})) || (rc = check_in_q(a.q, a.out, tokens)))
     return rc;
   hipError_t e = launch_history(a, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return hip_fail(e, "attention of histories");
@@ -379,7 +387,9 @@ int emb_history_step(emb_history* history, emb_kv* kv, int32_t seqs, const void*
                     {out, out_token_stride, out_head_stride, h.q_heads}, lens, table, table_width, bias, lse, parts,
                     static_cast<float*>(ws),
                     reinterpret_cast<float*>(static_cast<char*>(ws) + step_lse_offset(h, parts, seqs))};
-  if ((rc = check_wide("q", a.q, seqs, h, false)) || (rc = check_wide("out", a.out, seqs, h, true))) return rc;
+  if ((rc = check_wide("q", a.q, seqs, h, false)) || (rc = check_wide("out", a.out, seqs, h, true)) ||
+      (rc = check_in_q(a.q, a.out, seqs)))
+    return rc;
   if ((rc = check_workspace(ws, ws_bytes, emb_history_step_workspace_bytes(history, kv, seqs, table_width)))) return rc;
   hipError_t e = launch_history_step(a, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return hip_fail(e, "attention of new items");

@@ -784,7 +784,8 @@ int emb_check_history_error(emb_history* history, void* hip_stream);
  * [tokens][q_heads] or NULL (the gradient needs it). bias: NULL if and only if
  * buckets is 0; 4-byte aligned, like lse. tokens < 2^24, seqs < 2^24, tokens *
  * q_heads < 2^31, (seqs + tokens / 64) * q_heads < 2^24, token strides < 2^24
- * elements; the gradient's limits are the same. */
+ * elements; the gradient's limits are the same. out may be q with the same
+ * strides. */
 int emb_history_attention(emb_history* history, int64_t tokens, const void* q, int64_t q_token_stride,
                           int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
                           const void* v, int64_t v_token_stride, int64_t v_head_stride, void* out,
@@ -818,8 +819,9 @@ int emb_history_attention_backward(emb_history* history, int64_t tokens, const v
  * -infinity. Bad pages and lengths raise the cache's error flag; table_width
  * bounds the split of the work, so it should not be much wider than needed.
  * q_heads is at most 32 times kv_heads; seqs * kv_heads < 2^23, seqs * q_heads <
- * 2^28. lse: fp32 [seqs][q_heads] or NULL. ws: device, 16-byte aligned, at least
- * emb_history_step_workspace_bytes (0 on invalid arguments). */
+ * 2^28. out may be q with the same strides. lse: fp32 [seqs][q_heads] or NULL.
+ * ws: device, 16-byte aligned, at least emb_history_step_workspace_bytes (0 on
+ * invalid arguments). */
 size_t emb_history_step_workspace_bytes(const emb_history* history, const emb_kv* kv, int32_t seqs,
                                         int32_t table_width);
 int emb_history_step(emb_history* history, emb_kv* kv, int32_t seqs, const void* q, int64_t q_token_stride,
