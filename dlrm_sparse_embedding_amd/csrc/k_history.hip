@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256, 2) void k_history(HistoryArgs a, int tiles, Fa
 #pragma unroll
     for (int d = 0; d < D / 32; ++d) w.o[d] = f16v{};
   }
-  if (__builtin_expect(marked, 0)) add_marks<D>(w.o, s_marks, place);
+  if (__builtin_expect(marked, 0) && some) add_marks<D>(w.o, s_marks, place);
   short* dst = reinterpret_cast<short*>(const_cast<void*>(a.out.p)) + token * a.out.ts + head * a.out.hs + 8 * (lane >> 5);
   store_columns<DT, D>(dst, w.o, inv, store);
 }

@@ -746,8 +746,9 @@ int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t
  * off by up to 6 * 2^-24 |s| relative, which at that magnitude is less than
  * half a step of bf16, and far beyond it any number.
  * Tokens that a query does not see have no influence on its row, whatever they
- * hold (other sequences', later ones'), except that hidden keys' infinities
- * enter products with a weight of 0. Reruns are bit-identical.
+ * hold (other sequences', later ones'). Keys that only the bias hides from it
+ * should hold numbers: an infinity or NaN there can reach its output, if it
+ * sees others, and its gradients. Reruns are bit-identical.
  * EMB_BF16 / EMB_F16 heads of dim 64, 96 or 128; operands 16-byte aligned, their
  * strides multiples of 16 bytes. Softmax statistics, scores and sums are fp32;
  * probabilities and score gradients are rounded to the heads' type for the
