@@ -697,14 +697,29 @@ def emb_dropout(x, y, p: float, seed: int, step=None, residual=None, stream=None
                              _stream_for(x, stream)))
 
 
+# What a handle stands for, so that operands can be checked: q heads, k heads, dim, type, rows of the bias.
+_histories = {}
+
+
 def emb_create_history(desc: emb_history_desc) -> int:
     out = ctypes.c_void_p()
     _check(lib().emb_create_history(ctypes.byref(desc), ctypes.byref(out)))
+    _histories[out.value] = (desc.q_heads, desc.kv_heads, desc.dim,
+                             torch.bfloat16 if desc.dtype == EMB_BF16 else torch.float16,
+                             desc.buckets * (1 if desc.causal else 2))
     return out.value
 
 
 def emb_destroy_history(history: int) -> None:
+    _histories.pop(history, None)
     lib().emb_destroy_history(history)
+
+
+def _history(history):
+    dims = _histories.get(history)
+    if dims is None:
+        raise ValueError("history is not a handle of emb_create_history, or was destroyed")
+    return dims
 
 
 def emb_check_history_error(history: int, stream=None) -> None:
@@ -734,10 +749,6 @@ def _offsets(offsets):
     return _dense("offsets", offsets, torch.int32, offsets.shape), offsets.shape[0] - 1
 
 
-# What a handle stands for, so that operands can be checked: q heads, k heads, dim, type, rows of the bias.
-_histories = {}
-
-
 def _bias(name: str, bias, dims):
     return None if bias is None else _dense(name, bias, torch.float32, (dims[4], dims[0]))
 
@@ -745,7 +756,7 @@ def _bias(name: str, bias, dims):
 def emb_history_attention(history: int, q, k, v, out, offsets, bias=None, lse=None, stream=None) -> None:
     """q, out: [tokens, q_heads, dim]; k, v: [tokens, kv_heads, dim]; offsets: int32 [seqs + 1]; bias: fp32 [rows,
     q_heads], given if and only if the history has buckets; lse: fp32 [tokens, q_heads] or None."""
-    dims = _histories[history]
+    dims = _history(history)
     T, args = _ragged(q, k, v, dims[:4])
     off, B = _offsets(offsets)
     _check(lib().emb_history_attention(
@@ -760,7 +771,7 @@ def emb_history_attention_workspace_bytes(history: int, tokens: int, seqs: int) 
 def emb_history_attention_backward(history: int, q, k, v, out, lse, dout, dq, dk, dv, offsets, ws, bias=None,
                                    dbias=None, stream=None) -> None:
     """Gradients of emb_history_attention from its inputs, out and lse: dq, dk, dv and, where given, dbias."""
-    dims = _histories[history]
+    dims = _history(history)
     T, args = _ragged(q, k, v, dims[:4])
     off, B = _offsets(offsets)
     ws_p, ws_n = _workspace(ws)
@@ -777,7 +788,7 @@ def emb_history_step_workspace_bytes(history: int, kv: int, seqs: int, table_wid
 def emb_history_step(history: int, kv: int, q, out, lens, table, ws, bias=None, lse=None, stream=None) -> None:
     """q, out: [seqs, q_heads, dim], a query for each sequence at its newest slot; lens: int32 [seqs]; table: int32
     [seqs, pages]."""
-    dims = _histories[history]
+    dims = _history(history)
     hq, _, D, dtype, _ = dims
     if q.dim() != 3 or q.shape[1] != hq:
         raise ValueError(f"q has shape {tuple(q.shape)}, not [seqs, {hq}, {D}]")
@@ -866,11 +877,9 @@ class HistoryAttention:
         self.handle = emb_create_history(emb_history_desc(q_heads, kv_heads, dim, DTYPE_CODE[dtype], 1 if causal else 0,
                                                           buckets, exact, far, scale, 0, self.error.data_ptr()))
         self.bias_rows = buckets if causal else 2 * buckets
-        _histories[self.handle] = (q_heads, kv_heads, dim, TORCH_DTYPE[dtype], self.bias_rows)
 
     def close(self) -> None:
         if self.handle:
-            _histories.pop(self.handle, None)
             emb_destroy_history(self.handle)
             self.handle = None
 
