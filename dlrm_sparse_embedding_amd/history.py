@@ -20,7 +20,7 @@ from .ranking import Pages
 
 class HistoryEncoder(Pages):
     """One layer over embedded items. A distance of `exact` items and more shares its bias with others, from near `far`
-    on with all (emb.HistoryAttention). Its weights are fp32, those of the two projections with a rounded copy."""
+    on with all (emb.HistoryAttention); with no buckets there is no bias. Its weights are fp32, those of the two projections with a rounded copy."""
 
     def __init__(self, items: int, width: int = 128, heads: int = 8, kv_heads: int = 2, dim: int = 64,
                  buckets: int = 32, exact: int = 16, far: int = 1024, dropout: float = 0.1, pages: int = 1024,
@@ -36,7 +36,7 @@ class HistoryEncoder(Pages):
         self.back_master = torch.randn((heads * dim, width), generator=gen, device="cuda").mul_(1 / math.sqrt(heads * dim))
         self.proj, self.back = self.master.to(dtype), self.back_master.to(dtype)
         self.attention = E.HistoryAttention(heads, kv_heads, dim, "bf16" if dtype == torch.bfloat16 else "f16",
-                                            buckets=buckets, exact=exact, far=far)
+                                            buckets=buckets, exact=exact if buckets else 0, far=far if buckets else 0)
         self.bias = torch.zeros((self.attention.bias_rows, heads), device="cuda") if buckets else None
         self.count = torch.zeros(1, dtype=torch.int64, device="cuda")     # training steps taken: dropout's step
         self.hold_cache(pages, page, kv_heads, dim, dtype)
