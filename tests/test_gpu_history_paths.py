@@ -1,11 +1,13 @@
 """GPU tests of paths of the attention of histories and its gradient that short or narrow cases do not take: whole
 64-query halves of the gradient's tiles (bf16 heads of 96 and 128) with biases of each distance and of both directions'
-last buckets, and several key tiles in both directions. Tolerances as in test_gpu_history.py."""
+last buckets, several key tiles in both directions, and the correction of the rows' sums.
+Tolerances as in test_gpu_history.py, but for the correction's test, which derives its own."""
+import numpy as np
 import pytest
 import torch
 
 from oracle import history_oracle as H
-from tests.test_gpu_history import Call
+from tests.test_gpu_history import Call, U, close, half, n64
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,46 @@ def test_whole_halves_of_tiles(dt, dim, hq, hk, lens, causal, spec):
         c.backward()
         assert torch.equal(c.dbias, dbias)
     c.h.check_error()
+
+
+@pytest.mark.parametrize("dt,dim,causal,spec", [
+    ("bf16", 64, True, None), ("bf16", 64, False, LAST), ("bf16", 96, True, LAST), ("bf16", 128, True, LAST),
+    ("bf16", 128, False, None)])
+def test_gradient_of_queries_is_corrected_for_the_rounding_of_out(dt, dim, causal, spec):
+    """Values and keys with a large part in common: rounding `out` to its type moves dout . out, with which a row's sum
+    of P dP starts, by about as much as dS itself, and a dq made from that sum by `mistake` = scale (dout . (out - its
+    exact value)) sum P k. After the correction there remain, with h half a step of the type, slip the size of that
+    shift, and per row over its keys:
+      - dS, shift included, rounded for the product: h (sum |dS| |k| + slip sum P |k|);
+      - P rounded in the product that is taken off: h slip sum P |k|;
+      - P off by 2 e relative through the scores: 2 e (sum |dS| |k| + sum |dS| sum P |k|);
+      - dP and the sums in fp32: (D + 600) u sum P (|dP| + sum P |dP|) |k|, |.| magnitudes; and h of the result."""
+    n = 200
+    c = Call(dt, dim, 2, 1, [n], causal, spec, "plain")
+    gen = torch.Generator().manual_seed(dim)
+    for t, by in ((c.v, 16.0), (c.k, 3.0)):
+        t.copy_(t.float() + by * (1 + torch.rand((1, 1, dim), generator=gen)).cuda())
+    c.forward()
+    c.backward()
+    q, k, v = c.arrays()
+    do, out, bias = n64(c.dout), n64(c.out), n64(c.bias)
+    want = np.zeros_like(do)
+    tol, mistake = np.zeros_like(do), np.zeros_like(do)
+    h, e = half(dt), c.score_error()
+    for i in range(2):
+        s, _ = H.scores(q[:, i], k[:, 0], c.scale, causal, None if bias is None else bias[:, i], spec)
+        p, _ = H.softmax(s)
+        dp, adp = do[:, i] @ v[:, 0].T, np.abs(do[:, i]) @ np.abs(v[:, 0]).T
+        ds = p * (dp - (p * dp).sum(1, keepdims=True))
+        mag = p * (adp + (p * adp).sum(1, keepdims=True))
+        ak = np.abs(k[:, 0])
+        off = (do[:, i] * (out[:, i] - p @ v[:, 0])).sum(1, keepdims=True)
+        slip, pk = np.abs(off), p @ ak
+        want[:, i] = c.scale * (ds @ k[:, 0])
+        mistake[:, i] = c.scale * np.abs(off * (p @ k[:, 0]))
+        tol[:, i] = c.scale * (h * (np.abs(ds) @ ak + 2 * slip * pk) +
+                               2 * e * (np.abs(ds) @ ak + np.abs(ds).sum(1, keepdims=True) * pk) +
+                               (dim + 600) * U * (mag @ ak))
+    tol += h * np.abs(want)
+    assert (mistake > 2 * tol).mean() > 0.05         # a dq without the correction would show
+    close(c.dq, want, tol, dt, "dq")
