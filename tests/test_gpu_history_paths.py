@@ -1,6 +1,6 @@
 """GPU tests of paths of the attention of histories and its gradient that short or narrow cases do not take: whole
 64-query halves of the gradient's tiles (bf16 heads of 96 and 128) with biases of each distance and of both directions'
-last buckets, several key tiles in both directions, and the correction of the rows' sums.
+last buckets, several key tiles in both directions, the correction of the rows' sums, and the largest strides.
 Tolerances as in test_gpu_history.py, but for the correction's test, which derives its own."""
 import numpy as np
 import pytest
@@ -110,3 +110,21 @@ def test_gradient_of_queries_is_corrected_for_the_rounding_of_out(dt, dim, causa
     tol += h * np.abs(want)
     assert (mistake > 2 * tol).mean() > 0.05         # a dq without the correction would show
     close(c.dq, want, tol, dt, "dq")
+
+
+def test_the_largest_strides():
+    """Tokens 2^24 - 8 elements apart, the most that a call takes: the rows of a tile span nearly 2^32 bytes."""
+    n, ts = 170, (1 << 24) - 8
+    for dim, spec in ((64, (32, 16, 128)), (128, None)):
+        c = Call("bf16", dim, 1, 1, [n], True, spec, "plain")
+        c.forward(), c.backward()
+        want = [t.clone() for t in (c.out, c.lse, c.dq, c.dk, c.dv)]
+        dbias = None if spec is None else c.dbias.clone()
+        base = torch.empty(n * ts, dtype=torch.bfloat16, device="cuda")
+        far = [base.as_strided((n, 1, dim), (ts, dim, 1), dim * i) for i in range(8)]
+        for x, t in zip(far, (c.q, c.k, c.v, c.dout)):
+            x.copy_(t)
+        c.q, c.k, c.v, c.dout, c.out, c.dq, c.dk, c.dv = far
+        c.forward(), c.backward()
+        assert all(torch.equal(x, y) for x, y in zip(want, (c.out, c.lse, c.dq, c.dk, c.dv)))
+        assert dbias is None or torch.equal(dbias, c.dbias)
