@@ -421,6 +421,7 @@ template <int DT, int D, bool BIAS, bool NEAR>
 __device__ __forceinline__ void dkv_pair(const BackDev& p, KeyWave<DT, D>& w, const BiasLds& sb, float (*win)[64],
                                          GradLds<BIAS>& g, float (&far)[2], const TileLane<D>& tl, const short* qs,
                                          const short* gs, const float* zs, const float* deltas, int q0, int k0) {
+  static_assert(DT == EMB_BF16, "dS goes into its product without a scale");
   RowOps<D> qr, gr;
   ColumnOps<D> gc, qc;
   qr.read(tl, qs);
@@ -444,36 +445,18 @@ __device__ __forceinline__ void dkv_pair(const BackDev& p, KeyWave<DT, D>& w, co
   dkv_weights<DT, NEAR>(p.scale2, b[0].value, win[0], zs, deltas, s[0], dp[0], xp);
   interleave<D / 8, 8>();
   stage();
-  if constexpr (DT != EMB_F16) {
-    qc.read(tl, qs);
-    pack_tile<DT>(dp[0], xs[0]);
-    gc.template times<DT>(w.dv, xp);
-    gc.read(tl, gs + 32 * D);
-    qc.template times<DT>(w.dk, xs[0]);
-    dkv_weights<DT, NEAR>(p.scale2, b[1].value, win[1], zs + 32, deltas + 32, s[1], dp[1], xp);
-    interleave<D / 8, 8>();
-    stage();
-    qc.read(tl, qs + 32 * D);
-    pack_tile<DT>(dp[1], xs[1]);
-    gc.template times<DT>(w.dv, xp);
-    qc.template times<DT>(w.dk, xs[1]);
-  } else {
-    // both halves' dS go by one scale, chosen when both are there
-    gc.template times<DT>(w.dv, xp);
-    gc.read(tl, gs + 32 * D);
-    dkv_weights<DT, NEAR>(p.scale2, b[1].value, win[1], zs + 32, deltas + 32, s[1], dp[1], xp);
-    interleave<D / 16, 16>();
-    stage();
-    qc.read(tl, qs);
-    gc.template times<DT>(w.dv, xp);
-    w.c.fit(dp[0], w.dk);
-    w.c.fit(dp[1], w.dk);
-    pack_tile<DT>(w.c.scaled(dp[0]), xs[0]);
-    pack_tile<DT>(w.c.scaled(dp[1]), xs[1]);
-    qc.template times<DT>(w.dk, xs[0]);
-    qc.read(tl, qs + 32 * D);
-    qc.template times<DT>(w.dk, xs[1]);
-  }
+  qc.read(tl, qs);
+  pack_tile<DT>(dp[0], xs[0]);
+  gc.template times<DT>(w.dv, xp);
+  gc.read(tl, gs + 32 * D);
+  qc.template times<DT>(w.dk, xs[0]);
+  dkv_weights<DT, NEAR>(p.scale2, b[1].value, win[1], zs + 32, deltas + 32, s[1], dp[1], xp);
+  interleave<D / 8, 8>();
+  stage();
+  qc.read(tl, qs + 32 * D);
+  pack_tile<DT>(dp[1], xs[1]);
+  gc.template times<DT>(w.dv, xp);
+  qc.template times<DT>(w.dk, xs[1]);
   add_dbias<BIAS>(p, b[0], dp[0], g, far);
   add_dbias<BIAS>(p, b[1], dp[1], g, far);
 }
