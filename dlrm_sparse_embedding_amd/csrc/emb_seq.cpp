@@ -36,10 +36,11 @@ int check_heads(const char* name, const Heads& h, int dtype) {
 // An operand that is written: no two of its heads may share elements.
 int check_out(const char* name, const Heads& h, long long tokens, int dim, int dtype) {
   if (int rc = check_heads(name, h, dtype)) return rc;
+  typedef __int128 Wide;  // strides may be anything up to 2^63
   const bool heads_apart = h.n <= 1 || h.hs >= dim;
-  const bool tokens_apart = tokens <= 1 || h.ts >= (h.n - 1) * h.hs + dim;
+  const bool tokens_apart = tokens <= 1 || h.ts >= (Wide)(h.n - 1) * h.hs + dim;
   // tokens inside heads: [heads][tokens][dim] in memory
-  const bool swapped = (tokens <= 1 || h.ts >= dim) && (h.n <= 1 || h.hs >= (tokens - 1) * h.ts + dim);
+  const bool swapped = (tokens <= 1 || h.ts >= dim) && (h.n <= 1 || h.hs >= (Wide)(tokens - 1) * h.ts + dim);
   if (!((heads_apart && tokens_apart) || swapped))
     return fail(EMB_E_INVAL, "%s: heads of strides %lld, %lld overlap", name, h.ts, h.hs);
   return EMB_OK;
