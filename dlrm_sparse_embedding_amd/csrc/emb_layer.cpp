@@ -385,12 +385,12 @@ int emb_history_step(emb_history* history, emb_kv* kv, int32_t seqs, const void*
   const int parts = history_step_parts(h, kv->v, seqs, table_width);
   HistoryStepArgs a{h, kv->v, seqs, {q, q_token_stride, q_head_stride, h.q_heads},
                     {out, out_token_stride, out_head_stride, h.q_heads}, lens, table, table_width, bias, lse, parts,
-                    static_cast<float*>(ws),
-                    reinterpret_cast<float*>(static_cast<char*>(ws) + step_lse_offset(h, parts, seqs))};
+                    static_cast<float*>(ws), nullptr};
   if ((rc = check_wide("q", a.q, seqs, h, false)) || (rc = check_wide("out", a.out, seqs, h, true)) ||
       (rc = check_in_q(a.q, a.out, seqs)))
     return rc;
   if ((rc = check_workspace(ws, ws_bytes, emb_history_step_workspace_bytes(history, kv, seqs, table_width)))) return rc;
+  a.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + step_lse_offset(h, parts, seqs));
   hipError_t e = launch_history_step(a, static_cast<hipStream_t>(hip_stream));
   if (e != hipSuccess) return hip_fail(e, "attention of new items");
   return ok();

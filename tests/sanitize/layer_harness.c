@@ -181,6 +181,10 @@ static int step(void) {
                               seqs[i] ? FAKE(6) : NULL, SIZE_MAX, NULL, NULL), valid ? EMB_OK : EMB_E_INVAL);
       CHECK(stub_launches() - before == (valid && seqs[i] > 0));
     }
+  EXPECT(emb_history_step(h, kv, 4, FAKE(1), 512, 64, FAKE(2), 512, 64, FAKE(3), FAKE(4), 8, FAKE(5), NULL, 1 << 20, NULL,
+                          NULL), EMB_E_INVAL);
+  EXPECT(emb_history_step(h, kv, 4, FAKE(1), 512, 64, FAKE(2), 512, 64, FAKE(3), FAKE(4), 8, FAKE(5), FAKE(6), 8, NULL,
+                          NULL), EMB_E_WORKSPACE);
   emb_destroy_kv(kv);
   emb_destroy_history(h);
   return 0;
