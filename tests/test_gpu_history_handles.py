@@ -29,3 +29,39 @@ def test_a_created_handle_gives_the_same_bits():
     E.emb_check_history_error(mine[0])
     for h in mine:
         E.emb_destroy_history(h)
+
+
+def test_the_step_of_a_history_of_both_directions():
+    """A new item sees earlier ones only: the rows of the other direction have no part in its step."""
+    s = Step("bf16", 64, 4, 2, [300, 1, 40], 16, SPEC)
+    s.run()
+    want = [s.out.clone(), s.lse.clone()]
+    both = E.HistoryAttention(4, 2, 64, "bf16", causal=False, buckets=SPEC[0], exact=SPEC[1], far=SPEC[2])
+    s.bias = torch.cat([s.bias, torch.full_like(s.bias, float("nan"))])
+    s.h, old = both, s.h
+    s.run()
+    assert torch.equal(s.out, want[0]) and torch.equal(s.lse, want[1])
+    old.close()
+
+
+def test_two_graphs_that_share_a_workspace():
+    """Replayed in turn on one stream, with eager work on the same workspace between."""
+    a, b = Call("bf16", 64, 4, 2, [300, 77], True, SPEC, seed=1), Call("f16", 128, 2, 1, [129], False, SPEC, seed=2)
+    ws = max(a.ws, b.ws, key=lambda t: t.numel())
+    want, graphs = [], []
+    for c in (a, b):
+        want.append([t.clone() for t in [*c.forward(), *c.backward()]])
+        c.ws = ws
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            c.forward(), c.backward()
+    for i in (0, 1, 1, 0, 0, 1):
+        c = (a, b)[i]
+        got = [c.out, c.lse, c.dq, c.dk, c.dv, c.dbias]
+        for t in got:
+            t.fill_(3)
+        graphs[i].replay()
+        assert all(torch.equal(x, y) for x, y in zip(got, want[i]))
+        (b, a)[i].backward()
+        torch.cuda.synchronize()
