@@ -679,10 +679,11 @@ int emb_prefix_attention(emb_kv* kv, int64_t tokens, int32_t dtype, int32_t dim,
  * x_dtype is x's type, y_dtype that of y: the same, or EMB_BF16 / EMB_F16 for
  * an EMB_F32 x (rows of a table on their way to a 16-bit product). Rows are
  * read once; mean and variance are fp32, the variance of the differences from
- * the mean. y may be x with the same type and stride. 1 <= dim <=
- * EMB_MAX_ROW_DIM, rows < 2^31, eps finite and >= 0. Rows of 16-byte aligned
- * operands whose dim and strides are multiples of 16 bytes run at the memory's
- * rate, others element by element. */
+ * the mean (sums of squares beyond fp32's range give y = b). y may be x with
+ * the same type and stride. 1 <= dim <= EMB_MAX_ROW_DIM, rows < 2^31, eps finite
+ * and >= 0. Rows of 16-byte aligned operands whose dim and strides are multiples
+ * of 16 bytes, of up to 1024 columns, run at the memory's rate; others take up to
+ * twice as long. */
 int emb_layer_norm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype, int64_t x_stride, void* y,
                    int32_t y_dtype, int64_t y_stride, const float* w, const float* b, float eps, void* hip_stream);
 
@@ -736,7 +737,7 @@ int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t
  * buckets widen evenly on a logarithmic scale and the last one holds all
  * distances from near `far` on. row(d) = bucket(d) for d >= 0 and, without
  * causal, buckets + bucket(-d) for d < 0, so the table has `buckets` rows or 2
- * buckets (row `buckets` is then never used). exact = buckets: distances beyond
+ * buckets (row `buckets` is then never used, unless buckets is 1). exact = buckets: distances beyond
  * buckets - 1 share the last bucket, far is not used. buckets = 0: no bias.
  * An entry at or below EMB_HIDDEN_BIAS (-infinity, a 16- or 32-bit type's
  * lowest value, -1e4, -1e9) hides its distances: their keys are not seen. A
