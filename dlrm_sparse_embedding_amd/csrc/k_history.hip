@@ -14,11 +14,11 @@
 // and its probabilities already lie as the operand of O^T = V^T P^T.
 //
 // Bound by the products and the vector work of a wave, which overlap with another
-// wave's only in part: 12289 items, 16 x 4 heads of 128, causal, 270 us without a
-// bias (860 TFLOP/s), 305 with one of 64 buckets up to 1024, where a third of the
-// tiles have a bias for each diagonal (297 with the biases of all near distances in
-// a table, whose kernels for the gradient are slower); heads of 64 165 us (710 TFLOP/s: as many
-// exponentials for half the products). Waits that the compiler puts into the loop
+// wave's only in part: 12289 items, 16 x 4 heads of 128, causal, 267 us without a
+// bias (870 TFLOP/s), 306 with one of 64 buckets up to 1024, where a third of the
+// tiles have a bias for each diagonal, which each wave works out for itself (297
+// with the biases of all near distances in a table, not taken up); heads of 64
+// 164 us (714 TFLOP/s: as many exponentials for half the products). Waits that the compiler puts into the loop
 // (operands not there before it, spilled registers) also wait for the next tile's
 // transfer: without them the long cases went from 1137 to 1090 us.
 //

@@ -9,12 +9,14 @@
 // one order, without atomics.
 //
 // Bound by vector work and waits between products: 12289 items, 16 x 4 heads of
-// 128 bf16, causal: 1190 us (490 TFLOP/s of the five products that it needs; eight
-// are made), 1610 with the bias' gradient, 1445 without that but with a bias; dq
-// is about 490 of them. Heads of 64: 630 us; 128 users of up to 620 items, 8 x 2
-// heads: 386 with the bias' gradient, 331 without, 257 without a bias. Two blocks
-// a CU are worth more than registers: dq of 128-wide heads, 32 registers spilled
-// outside its loop, took 150 us less than with one block and none.
+// 128 bf16, causal: 1180 us (495 TFLOP/s of the five products that it needs; eight
+// are made), 1608 with the bias' gradient, 1444 without that but with a bias; dq
+// is about 490 of them. Heads of 64: 628 us; 128 users of up to 620 items, 8 x 2
+// heads: 389 with the bias' gradient, 332 without, 258 without a bias. Two blocks
+// a CU are worth more than registers: dq of 128-wide heads, which spills 9 (bf16) to
+// 25 registers (fp16 with a bias) and fetches a few of them back in its loop, took
+// 150 us less than with one block and none. dk and dv of 128-wide bf16 heads with a
+// bias spill 35 outside the loop over the tiles, of 64-wide fp16 ones with a bias 5.
 //
 // The rows' sums. sum_j P_ij dP_ij is dout_i . out_i but for the rounding of out,
 // which is enough for 16-bit results but not for dbias: its fp32 sums cancel (dS
@@ -469,9 +471,10 @@ __device__ __forceinline__ float wave_sum(float x) {
 
 // Whole tiles in pairs of half tiles, with one block a CU, or every half tile by
 // itself. The gradient of 12289 items, 16 x 4 heads, with a bias: 128 wide bf16
-// 1657 us in pairs and 1922 without (then); fp16, whose pairs take one scale and with it
-// more registers than there are, 2600 and 1705; 64 wide, where two blocks fit
-// without pairs, 696 and 632 (no bias).
+// 1657 us in pairs and 1922 without; fp16, whose pairs would need one scale for both
+// halves and with it more registers than there are, 2600 and 1705; 64 wide, where two
+// blocks fit without pairs, 696 and 632 (no bias). (Each pair as measured then; now
+// 1608, 1705 and 628.)
 template <int DT, int D>
 constexpr bool kPairs = D > 64 && DT == EMB_BF16;
 

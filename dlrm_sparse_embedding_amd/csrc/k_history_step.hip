@@ -8,8 +8,9 @@
 // their pages are looked up another tile ahead. Long histories are split into
 // parts, which a second launch joins with the weights 2^(z_i - max z). It is bound
 // by reading the slots once: 61 users of up to 3000 slots, 32 x 8 heads of 128
-// bf16, 90 us, 4.6 TB/s (76 where a part of them is still in the last cache); one user of 60001, 16 x 4 heads of 64 fp16, 20 us, of
-// which the join is 5 and the rest bound by dependent reads (length, page, slot).
+// bf16, 90 us, 4.6 TB/s (75 on the same inputs again, a part of which is still in the
+// last cache); one user of 60001, 16 x 4 heads of 64 fp16, 20 us, of which the join is
+// 5 and the rest bound by dependent reads (length, page, slot).
 #include <algorithm>
 
 #include "history_device.h"
@@ -314,9 +315,13 @@ hipError_t launch(const StepDev& p, hipStream_t st) {
 
 }  // namespace
 
-// Parts of the slots: two blocks for each CU at least, but none below 256 slots,
-// since each part writes and reads back an fp32 partial output. (61 users' 488
-// pairs with a head: 118 us for at least 1024 blocks, 128 for 600, 124 for 2048.)
+// Parts of the slots, by the table's width, since lengths are on the device: as many
+// as make 1024 blocks, but no more than the width has runs of 256 slots, since each
+// part writes and reads back an fp32 partial output. A sequence shorter than the
+// width has parts of whole rounds of the four waves, 128 slots, and empty ones. (61
+// users of up to 3000 slots, 488 pairs with a head: 89 us, 95 for 600 blocks, 96 for
+// 1500, 97 for 2048; 200 users of up to 1000: 88, 88, 88 and 114; 4 of up to 20000:
+// 45, 43, 50 and 56.)
 int history_step_parts(const HistoryView& h, const KvView& kv, int seqs, int width) {
   const long long items = (long long)seqs * h.kv_heads, cap = (long long)width * kv.page;
   if (items == 0) return 1;

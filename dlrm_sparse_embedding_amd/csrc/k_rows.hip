@@ -10,8 +10,13 @@
 // the rows of a group of lanes, in fp64 over the blocks, always in one order.
 // Measured: fp32 rows of 262144 x 128 normed to bf16 36 us (5.6 TB/s); gradient of
 // 24577 x 1024 bf16 30 us (5.0 TB/s) and 4 for the weights' sums over the blocks;
-// dropout and sum of 32768 x 1024 bf16 35 us (5.8 TB/s): its two Philox draws for
-// eight elements fit beside the memory's time.
+// dropout and sum of 32768 x 1024 bf16 35 us (5.8 TB/s): its Philox draw for eight
+// elements, and a second one where bits tie (one unit of eight in 8000), fit beside
+// the memory's time. Gradient of fp32 rows with 16-bit dy, as a table's are: 262144
+// x 128 66 us (5.1 TB/s), 24577 x 512 31 us (4.1 TB/s, 24 without the weights' sums).
+// Beyond 1024 columns it is further off: 6000 x 4096 bf16 47 us (3.1 TB/s), for the
+// barriers of a row's waves and, in blocks of 1024 threads, 128 registers, which do
+// not hold a row without spilling 4 to 15; off 16-byte borders 16 to 57.
 //
 // Layout. A row belongs to a group of G lanes (a power of two, at most a wave)
 // or, beyond 1024 columns, to 4 or 16 waves; lane u holds the columns E (k G + u) ..

@@ -77,6 +77,8 @@ class HistoryEncoder(Pages):
         lse = torch.empty(out.shape[:2], device="cuda")
         E.emb_history_attention(self.attention.handle, *self.parts(fused), out, offsets, bias=self.bias, lse=lse)
         y = out.flatten(1) @ self.back
+        # the rows join in the layer's type, as dropout takes operands of one type: half a step of them, next to that of
+        # the sum, which is stored in it anyway
         E.emb_dropout(y, y, self.dropout if train else 0.0, self.seed, step=self.count, residual=rows.to(self.dtype))
         return y, (rows, offsets, normed, fused, out, lse)
 
