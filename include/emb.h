@@ -745,7 +745,7 @@ int emb_dropout(int64_t rows, int32_t dim, int32_t dtype, const void* x, int64_t
  * Other entries and the scores must stay below -EMB_HIDDEN_BIAS in magnitude:
  * the gradient makes its weights from s and lse, whose fp32 roundings put them
  * off by up to 6 * 2^-24 |s| relative, which at that magnitude is less than
- * half a step of bf16, and far beyond it any number.
+ * half a step of bf16 (of fp16 up to 1365), and far beyond it any number.
  * Tokens that a query does not see have no influence on its row, whatever they
  * hold (other sequences', later ones'). Keys that only the bias hides from it
  * should hold numbers: an infinity or NaN there can reach its output, if it
